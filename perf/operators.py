@@ -319,7 +319,7 @@ def _plan(s):
     need = n.clamp(max=P)
     more = ((length + need + page - 1) // page - pages).clamp(min=0)
     before = more.cumsum(0) - more
-    fits = before + more <= s["free_pages"].numel() - s["free_head"].long()
+    fits = (more == 0) | (before + more <= s["free_pages"].numel() - s["free_head"].long())
     more = torch.where(fits, more, 0)
     j = torch.arange(table.shape[1], device=table.device)
     new = (j >= pages[:, None]) & (j < (pages + more)[:, None])
