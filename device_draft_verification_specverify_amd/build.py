@@ -8,10 +8,15 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCE = os.path.join(HERE, "csrc", "specverify.hip")
+# The operators on drafted token trees, a translation unit each.
+TREE_SOURCES = [os.path.join(HERE, "csrc", n)
+                for n in ("tree_cache.hip", "tree_verify.hip", "tree_attention.hip")]
 HOST_SOURCES = [os.path.join(HERE, "csrc", "bandit.cpp")]
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(HERE, "libspecverify.so")
@@ -41,14 +46,7 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (set HIPCC or install ROCm)")
 
 
-def build(verbose: bool = False, extra_flags: list[str] | None = None,
-          checked: bool = False) -> str:
-    """Compile the HIP source into LIBRARY, or CHECKED_LIBRARY with the device-side
-    index checks (always recompiles). Returns the path."""
-    out = CHECKED_LIBRARY if checked else LIBRARY
-    tmp = out + ".tmp"
-    flags = [*HIP_FLAGS, *(extra_flags or []), *(["-DSV_DEVICE_CHECKS"] if checked else [])]
-    cmd = [hipcc(), *flags, "-I", INCLUDE, SOURCE, *HOST_SOURCES, "-o", tmp]
+def _run(cmd: list[str], verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -56,6 +54,26 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None,
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
     if verbose and res.stderr.strip():
         print(res.stderr, file=sys.stderr)
+
+
+def build(verbose: bool = False, extra_flags: list[str] | None = None,
+          checked: bool = False) -> str:
+    """Compile the sources into LIBRARY, or CHECKED_LIBRARY with the device-side
+    index checks (always recompiles). Returns the path."""
+    out = CHECKED_LIBRARY if checked else LIBRARY
+    tmp = out + ".tmp"
+    flags = [*HIP_FLAGS, *(extra_flags or []), *(["-DSV_DEVICE_CHECKS"] if checked else [])]
+    with tempfile.TemporaryDirectory() as d:
+        # one compiler per source, side by side, then one link
+        units = [(src, os.path.join(d, os.path.basename(src) + ".o"))
+                 for src in [SOURCE, *TREE_SOURCES, *HOST_SOURCES]]
+        compile_flags = [f for f in flags if f != "-shared"]
+        cmds = [[hipcc(), *compile_flags, "-I", INCLUDE, "-c", src, "-o", obj]
+                for src, obj in units]
+        with ThreadPoolExecutor(max_workers=min(len(cmds), 8)) as ex:
+            list(ex.map(lambda c: _run(c, verbose), cmds))
+        _run([hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", *(obj for _, obj in units),
+              "-o", tmp], verbose)
     os.replace(tmp, out)
     return out
 
