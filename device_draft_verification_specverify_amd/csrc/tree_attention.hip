@@ -129,8 +129,30 @@ __device__ __forceinline__ uint64_t window(uint64_t m0, uint64_t m1, int x) {
   return x <= -64 ? ~uint64_t(0) : x < 0 ? some : x < 64 ? both : none;
 }
 
-// RW wavefronts along the rows (32 each), KW along a tile's keys (KB each).
-template <int DT, int DP, int RW, int KW, int KB>
+// 16 bytes a lane from global memory straight into LDS at `to` (the wavefront's
+// lanes in order). Written out because the compiler puts a wait for all such
+// loads in front of every later LDS read; the loop below counts them itself.
+__device__ __forceinline__ void load_lds16(const char* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(to), "v"(from)
+               : "memory", "m0");
+}
+
+// This wavefront's loads but the newest N have landed and its LDS reads are
+// done; then the workgroup meets.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(N) : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" : : : "memory");
+}
+
+constexpr int kTablePart = 1024;  // page ids held in LDS at a time
+
+// RW wavefronts along the rows (32 each), KW along a tile's keys (KB each), a
+// ring of S tiles.
+template <int DT, int DP, int RW, int KW, int KB, int S>
 __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   using E = Elem<DT>;
   using elem = typename E::type;
@@ -142,8 +164,11 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   constexpr int ND = DP / 32;
   constexpr int UNITS = KT * CPR / NT;
   static_assert(KT * CPR % NT == 0, "whole rounds of 16-byte pieces");
-  static_assert((KW - 1) * RW * ND * 16 * 64 * 4 <= 2 * KT * DP * 2, "the merge fits the tile");
-  __shared__ __align__(1024) char tile[2 * KT * DP * 2];
+  constexpr int STAGE = 2 * KT * DP * 2;  // bytes of a tile's keys and values
+  constexpr int LOADS = 2 * UNITS;        // of a thread for a tile
+  static_assert((KW - 1) * RW * ND * 16 * 64 * 4 <= S * STAGE, "the merge fits the tile");
+  __shared__ __align__(1024) char tile[S * STAGE];
+  __shared__ int32_t ids[kTablePart];
   __shared__ float merge_ml[KW][RW][2][32];
   __shared__ int64_t scan[NT / 64 + 1];
   __shared__ int64_t found[2];
@@ -209,8 +234,17 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   int64_t b_first = found[1];
   Req rq = request(a, b);
 
-  char* const tk = tile;
-  char* const tv = tile + KT * DP * 2;
+  // This lane's places in a stage. K: row col, piece 2 ks + half; V: 4 keys from
+  // 4 half on at 4 columns. Pieces are swizzled by their row, rows a multiple of
+  // 16 apart alike, and stages begin at multiples of 1024, so the ks-th piece
+  // and the db-th 32 columns are one exclusive or away.
+  const uint32_t k_off = (kw * KB + col) * (DP * 2) + ((half ^ swizzle<CPR>(col)) * 16);
+  const int v_row = 4 * half + ((lane & 15) >> 2);
+  const uint32_t v_off = KT * DP * 2 + (kw * KB + v_row) * (DP * 2) +
+                         (((((lane >> 4) & 1) * 2 + ((lane & 3) >> 1)) ^ swizzle<CPR>(v_row)) * 16) +
+                         (lane & 1) * 8;
+  const uint32_t tile_at = __builtin_amdgcn_readfirstlane(
+      uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)tile)));
   while (at < end) {
     while (at >= b_first + tiles_of(a, rq)) {
       b_first += tiles_of(a, rq);
@@ -256,40 +290,71 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
 #pragma unroll
     for (int i = 0; i < ND; ++i) acc[i] = f32x16{0};
     float m = -INFINITY, l = 0.0f;
+    int wild = 0;
 
-    for (int t = t0; t < t1; ++t) {
-      // the tile's keys and values into LDS, 16 bytes a lane
+    // Page ids of the share, a part at a time; bad ones become -1.
+    int ids_from = 0, ids_to = 0;  // pages held
+    auto fetch_ids = [&](int t) {
+      const int need = min(min(t * KT + KT, len) - 1, len - 1) >> a.page_shift;
+      if (len == 0 || t * KT >= len || need < ids_to) return;
+      __syncthreads();  // the ids before are read
+      ids_from = (t * KT) >> a.page_shift;
+      const int last = (min(t1 * KT, len) - 1) >> a.page_shift;
+      ids_to = min(ids_from + kTablePart, last + 1);
+      for (int i = tid; i < ids_to - ids_from; i += NT) {
+        int32_t id = table[ids_from + i];
+        if (id < 0 || id >= a.num_pages) {
+          set_error(a.err, SV_ERR_PAGE);
+          id = -1;
+        }
+        ids[i] = id;
+      }
+      __syncthreads();
+    };
+    // Starts a tile's keys and values on their way into stage t % S.
+    auto fetch = [&](int t) {
+      fetch_ids(t);
+      const uint32_t stage = tile_at + uint32_t(t % S) * STAGE;
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) {
-        const int unit = u * NT + tid;
-        const int row = unit / CPR;
-        const int c = (unit % CPR) ^ swizzle<CPR>(row);
+        const int row = u * (NT / CPR) + tid / CPR;
+        // rounds of 16 rows and more repeat the order of pieces
+        const int c = (tid % CPR) ^ swizzle<CPR>(NT / CPR % 16 == 0 ? tid / CPR : row);
         const int key = t * KT + row;
         const char* kp = reinterpret_cast<const char*>(&zero_piece);
         const char* vp = kp;
-        if (c * 8 < a.D && key < keys) {
+        if (c * 8 < a.D) {
           if (key < len) {
-            const int32_t id = table[key >> a.page_shift];
-            if (id >= 0 && id < a.num_pages) {
+            const int32_t id = ids[(key >> a.page_shift) - ids_from];
+            if (id >= 0) {
               kp = a.k_cache + id * a.c_page + (key & ((1 << a.page_shift) - 1)) * a.c_token +
                    h * a.c_h + c * 16;
               vp = kp + a.v_cache;
-            } else {
-              set_error(a.err, SV_ERR_PAGE);
             }
-          } else {
+          } else if (key < keys) {
             kp = a.k_tree + (rq.first + key - len) * a.n_t + h * a.n_h + c * 16;
             vp = kp + a.v_tree;
           }
         }
-        const int to = (u * NT + wv * 64) * 16;
-        __builtin_amdgcn_global_load_lds(GLOBAL_PTR(kp), LDS_PTR(tk + to), 16, 0, 0);
-        __builtin_amdgcn_global_load_lds(GLOBAL_PTR(vp), LDS_PTR(tv + to), 16, 0, 0);
+        const uint32_t to = stage + (u * NT + wv * 64) * 16;
+        load_lds16(kp, to);
+        load_lds16(vp, to + KT * DP * 2);
       }
-      __syncthreads();
+    };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i)
+      if (t0 + i < t1) fetch(t0 + i);
+
+    for (int t = t0; t < t1; ++t) {
+      // tile t is here; everyone is done with tile t - 1, whose stage is next
+      if (S >= 4 && t1 - t > 2) wait_and_meet<2 * LOADS>();
+      else if (S >= 3 && t1 - t > 1) wait_and_meet<LOADS>();
+      else wait_and_meet<0>();
+      if (t + S - 1 < t1) fetch(t + S - 1);
+      char* const tv = tile + (t % S) * STAGE + KT * DP * 2;
+      const uint32_t stage = tile_at + uint32_t(t % S) * STAGE;
       // Nodes' values that are infinite or NaN would reach the rows that do not
-      // see them as 0 * inf: they become zeros here and are added below.
-      int wild = 0;
+      // see them as 0 * inf: they become zeros here and are added at the end.
       if (t * KT + KT > len) {
         bool mine = false;
 #pragma unroll
@@ -310,19 +375,17 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
             mine = mine || any;
           }
         }
-        wild = __syncthreads_or(mine);
+        wild |= __syncthreads_or(mine);
       }
       if (wave_ok) {
         f32x16 s[NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           s[nb] = f32x16{0};
-          const int row = kw * KB + nb * 32 + col;
-          const char* kr = tk + row * (DP * 2);
 #pragma unroll
           for (int ks = 0; ks < DP / 16; ++ks) {
-            const s16x8 kf = *reinterpret_cast<const s16x8*>(
-                kr + (((2 * ks + half) ^ swizzle<CPR>(row)) * 16));
+            const s16x8 kf = *reinterpret_cast<__attribute__((address_space(3))) const s16x8*>(
+                (uint32_t(stage + k_off) ^ (ks * 32)) + nb * 32 * (DP * 2));
             s[nb] = E::mfma(kf, qf[ks], s[nb]);
           }
         }
@@ -366,52 +429,23 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) pf[j] = elem(s[nb][8 * ks + j]);
             // V^T: columns d of this lane, keys in the order of the scores
-            const int row = kw * KB + nb * 32 + ks * 16 + 4 * half + ((lane & 15) >> 2);
 #pragma unroll
             for (int db = 0; db < ND; ++db) {
-              const int d = db * 32 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
-              const int off = (d & 7) * 2;
-              const char* v0 =
-                  tv + row * (DP * 2) + (((d >> 3) ^ swizzle<CPR>(row)) * 16) + off;
-              const char* v1 =
-                  tv + (row + 8) * (DP * 2) + (((d >> 3) ^ swizzle<CPR>(row + 8)) * 16) + off;
+              const uint32_t at0 = (stage + v_off) ^ (db * 64);
+              const uint32_t at1 = (stage + (v_off ^ 32)) ^ (db * 64);
+              const uint32_t rows = (nb * 32 + ks * 16) * (DP * 2);
               const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                  (__attribute__((address_space(3))) s16x4*)(v0));
+                  (__attribute__((address_space(3))) s16x4*)(at0 + rows));
               const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                  (__attribute__((address_space(3))) s16x4*)(v1));
+                  (__attribute__((address_space(3))) s16x4*)(at1 + rows + 8 * (DP * 2)));
               const s16x8 vf = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
               acc[db] = E::mfma(vf, pf, acc[db]);
             }
           }
         }
-        if (wild) {
-          for (int k = 0; k < KB; ++k) {
-            const int x = t * KT + kw * KB + k - len;
-            if (x < 0 || x >= n) continue;
-            float pk = 0.0f;
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (nb == k / 32 && i == (k % 32) / 8 * 4 + k % 4) pk = s[nb][i];
-            pk = __shfl(pk, col + 32 * ((k >> 2) & 1));
-            const bool see = ((x < 64 ? see0 >> (x & 63) : see1 >> (x & 63)) & 1) != 0;
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(
-                a.k_tree + a.v_tree + (rq.first + x) * a.n_t + h * a.n_h);
-#pragma unroll
-            for (int i = 0; i < ND; ++i)
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int d = i * 32 + 8 * (j / 4) + 4 * half + j % 4;
-                const uint16_t raw = d < a.D ? v[d] : 0;
-                const float add = fmaxf(pk, 1e-30f) * float(__builtin_bit_cast(elem, raw));
-                acc[i][j] += see && E::wild(raw) ? add : 0.0f;
-              }
-          }
-        }
       }
-      __syncthreads();
     }
+    __syncthreads();
     l += __shfl_xor(l, 32);
 
     if constexpr (KW > 1) {
@@ -453,6 +487,33 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
       __syncthreads();
     }
 
+    if (wild && kw == 0) {
+      // The wild values of the nodes among this share's keys, for the rows that
+      // see them (rare, so scores are simply taken again).
+      for (int x = max(t0 * KT - len, 0); x < min(t1 * KT - len, n); ++x) {
+        const bool see = row_ok && ((x < 64 ? see0 >> (x & 63) : see1 >> (x & 63)) & 1);
+        const char* kp = a.k_tree + (rq.first + x) * a.n_t + h * a.n_h;
+        const elem* kx = reinterpret_cast<const elem*>(kp);
+        const elem* qx = reinterpret_cast<const elem*>(a.q + (rq.first + node) * a.q_t + hq * a.q_h);
+        const uint16_t* vx = reinterpret_cast<const uint16_t*>(kp + a.v_tree);
+        float dot = 0.0f;
+#pragma unroll 1
+        for (int d = 0; d < a.D; ++d) dot = fmaf(float(qx[d]), float(kx[d]), dot);
+        // a weight that underflows is still one
+        const float px = fmaxf(__builtin_amdgcn_exp2f(fmaf(dot, a.scale_log2, -m)), 1e-30f);
+#pragma unroll
+        for (int i = 0; i < ND; ++i)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int d = i * 32 + 8 * (j / 4) + 4 * half + j % 4;
+            const uint16_t raw = d < a.D ? vx[d] : 0;
+            const float sum = fmaf(px, float(__builtin_bit_cast(elem, raw)), acc[i][j]);
+            acc[i][j] = see & E::wild(raw) ? sum : acc[i][j];
+            __builtin_amdgcn_sched_barrier(0);  // few registers rather than many loads at once
+          }
+      }
+    }
+
     if (kw == 0 && row_ok) {
       if (t0 == 0 && t1 == rq.tiles) {
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
@@ -487,6 +548,8 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
         }
       }
     }
+    // Loads are counted in order among themselves only: no store stays behind.
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
     at += t1 - t0;
   }
 }
@@ -552,25 +615,37 @@ struct Variant {
 Variant variant_of(int64_t rows, int64_t D) {
   Variant v;
   v.width = D <= 64 ? 64 : D <= 128 ? 128 : 256;
-  v.rw = rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 ? 4 : 8;
-  v.kw = v.rw == 1 ? 4 : v.rw == 2 ? 2 : 1;
-  v.kb = v.kw == 4 || v.width == 256 ? 32 : 64;
-  v.workers = v.rw == 8 || v.width == 256 ? 256 : 512;
+  v.rw = rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 || v.width == 256 ? 4 : 8;
+  if (v.width == 256) {
+    v.kw = v.rw == 1 ? 2 : v.rw == 2 ? 2 : 1;
+    v.kb = 32;
+  } else {
+    v.kw = v.rw == 1 ? 4 : 8 / v.rw;
+    v.kb = v.rw == 8 ? 64 : 32;
+  }
+  v.workers = 256;
   return v;
+}
+
+template <int DT, int DP, int RW, int KW, int KB, int S>
+void launch_one(const Variant& v, const AttnArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((attention_kernel<DT, DP, RW, KW, KB, S>), dim3(unsigned(v.workers)),
+                     dim3(64 * RW * KW), 0, st, a);
 }
 
 template <int DT, int DP>
 void launch(const Variant& v, const AttnArgs& a, hipStream_t st) {
-  const dim3 grid{unsigned(v.workers)};
-  constexpr int KB = DP == 256 ? 32 : 64;
-  if (v.rw == 1)
-    hipLaunchKernelGGL((attention_kernel<DT, DP, 1, 4, 32>), grid, dim3(256), 0, st, a);
-  else if (v.rw == 2)
-    hipLaunchKernelGGL((attention_kernel<DT, DP, 2, 2, KB>), grid, dim3(256), 0, st, a);
-  else if (v.rw == 4)
-    hipLaunchKernelGGL((attention_kernel<DT, DP, 4, 1, KB>), grid, dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL((attention_kernel<DT, DP, 8, 1, KB>), grid, dim3(512), 0, st, a);
+  if constexpr (DP == 256) {
+    if (v.rw == 1) launch_one<DT, DP, 1, 2, 32, 2>(v, a, st);
+    else if (v.rw == 2) launch_one<DT, DP, 2, 2, 32, 2>(v, a, st);
+    else launch_one<DT, DP, 4, 1, 32, 4>(v, a, st);
+  } else {
+    constexpr int X = 128 / DP;  // stages of half the size, twice as many
+    if (v.rw == 1) launch_one<DT, DP, 1, 4, 32, 2 * X>(v, a, st);
+    else if (v.rw == 2) launch_one<DT, DP, 2, 4, 32, 2 * X>(v, a, st);
+    else if (v.rw == 4) launch_one<DT, DP, 4, 2, 32, 4>(v, a, st);
+    else launch_one<DT, DP, 8, 1, 64, 4>(v, a, st);
+  }
 }
 
 template <int DT>
