@@ -163,6 +163,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   constexpr int NB = KB / 32;
   constexpr int ND = DP / 32;
   constexpr int UNITS = KT * CPR / NT;
+  constexpr int STEP = DP / 16 < 8 ? DP / 16 : 8;  // fragments of K read at once
   static_assert(KT * CPR % NT == 0, "whole rounds of 16-byte pieces");
   constexpr int STAGE = 2 * KT * DP * 2;  // bytes of a tile's keys and values
   constexpr int LOADS = 2 * UNITS;        // of a thread for a tile
@@ -311,31 +312,45 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
       }
       __syncthreads();
     };
-    // Starts a tile's keys and values on their way into stage t % S.
+    // Starts a tile's keys and values on their way into stage t % S. Branches
+    // only where the whole workgroup takes them; lanes choose between addresses.
+    const char* const zero = reinterpret_cast<const char*>(&zero_piece);
+    const char* const k_head = a.k_cache + h * a.c_h;
+    const char* const k_node = a.k_tree + rq.first * a.n_t + h * a.n_h;
+    const int64_t c_page = a.c_page, c_token = a.c_token, v_cache = a.v_cache;
+    const int in_page = (1 << a.page_shift) - 1, page_shift = a.page_shift;
     auto fetch = [&](int t) {
       fetch_ids(t);
       const uint32_t stage = tile_at + uint32_t(t % S) * STAGE;
+      const int key0 = t * KT + tid / CPR;
+      const bool inside = t * KT + KT <= len;  // cached keys only
+      int32_t id[UNITS];
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int key = key0 + u * (NT / CPR);
+        const int at_id = (key >> page_shift) - ids_from;
+        id[u] = ids[inside || key < len ? at_id : 0];
+      }
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) {
         const int row = u * (NT / CPR) + tid / CPR;
         // rounds of 16 rows and more repeat the order of pieces
         const int c = (tid % CPR) ^ swizzle<CPR>(NT / CPR % 16 == 0 ? tid / CPR : row);
         const int key = t * KT + row;
-        const char* kp = reinterpret_cast<const char*>(&zero_piece);
-        const char* vp = kp;
-        if (c * 8 < a.D) {
-          if (key < len) {
-            const int32_t id = ids[(key >> a.page_shift) - ids_from];
-            if (id >= 0) {
-              kp = a.k_cache + id * a.c_page + (key & ((1 << a.page_shift) - 1)) * a.c_token +
-                   h * a.c_h + c * 16;
-              vp = kp + a.v_cache;
-            }
-          } else if (key < keys) {
-            kp = a.k_tree + (rq.first + key - len) * a.n_t + h * a.n_h + c * 16;
-            vp = kp + a.v_tree;
-          }
+        const char* kp = k_head + c * 16 + uint32_t(id[u]) * uint64_t(c_page) +
+                         uint32_t(key & in_page) * uint64_t(c_token);
+        bool some = id[u] >= 0;
+        const char* vp = kp + v_cache;
+        if (!inside) {
+          const char* np = k_node + c * 16 + int64_t(key - len) * a.n_t;
+          const char* nv = np + a.v_tree;
+          some = key < len ? some : key < keys;
+          kp = key < len ? kp : np;
+          vp = key < len ? vp : nv;
         }
+        some = some && (DP == a.D || c * 8 < a.D);
+        kp = some ? kp : zero;
+        vp = some ? vp : zero;
         const uint32_t to = stage + (u * NT + wv * 64) * 16;
         load_lds16(kp, to);
         load_lds16(vp, to + KT * DP * 2);
@@ -378,17 +393,42 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
         wild |= __syncthreads_or(mine);
       }
       if (wave_ok) {
+        // Fragments are read ahead of the products that take them, 8 at a time
+        // (the barriers keep the compiler from pulling each read down to its
+        // use, where its latency would show).
         f32x16 s[NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           s[nb] = f32x16{0};
 #pragma unroll
-          for (int ks = 0; ks < DP / 16; ++ks) {
-            const s16x8 kf = *reinterpret_cast<__attribute__((address_space(3))) const s16x8*>(
-                (uint32_t(stage + k_off) ^ (ks * 32)) + nb * 32 * (DP * 2));
-            s[nb] = E::mfma(kf, qf[ks], s[nb]);
+          for (int k8 = 0; k8 < DP / 16; k8 += STEP) {
+            s16x8 kf[STEP];
+#pragma unroll
+            for (int i = 0; i < STEP; ++i)
+              kf[i] = *reinterpret_cast<__attribute__((address_space(3))) const s16x8*>(
+                  ((stage + k_off) ^ ((k8 + i) * 32)) + nb * 32 * (DP * 2));
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) s[nb] = E::mfma(kf[i], qf[k8 + i], s[nb]);
           }
         }
+        // V^T of a half block of keys: columns d of this lane, keys in the order
+        // of the scores
+        s16x8 vf[2][STEP / 2];
+        auto read_v = [&](int half_block, int db0, s16x8* to) {
+#pragma unroll
+          for (int i = 0; i < STEP / 2; ++i) {
+            const uint32_t at = (stage + v_off) ^ ((db0 + i) * 64);
+            const uint32_t rows = half_block * 16 * (DP * 2);
+            const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)(at + rows));
+            const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4*)((at ^ 32) + rows + 8 * (DP * 2)));
+            to[i] = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
+          }
+        };
+        read_v(0, 0, vf[0]);
+        __builtin_amdgcn_sched_barrier(0);
         const int key0 = t * KT + kw * KB + 4 * half;
         if (t * KT + KT > len) {
           const uint64_t see = window(see0, see1, key0 - len);
@@ -417,31 +457,26 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
         }
         const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             s[nb][i] = __builtin_amdgcn_exp2f(fmaf(s[nb][i], a.scale_log2, -ref));
             l += s[nb][i];
           }
+        // V is read one step (a half block of keys, STEP / 2 blocks of columns)
+        // ahead of its products
+        constexpr int PER = ND / (STEP / 2), STEPS = 2 * NB * PER;
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            typename E::vec pf;
+        for (int st = 0; st < STEPS; ++st) {
+          const int hb = st / PER, db0 = st % PER * (STEP / 2);
+          if (st + 1 < STEPS) read_v((st + 1) / PER, (st + 1) % PER * (STEP / 2), vf[(st + 1) % 2]);
+          typename E::vec pf;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) pf[j] = elem(s[nb][8 * ks + j]);
-            // V^T: columns d of this lane, keys in the order of the scores
+          for (int j = 0; j < 8; ++j) pf[j] = elem(s[hb / 2][8 * (hb % 2) + j]);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int db = 0; db < ND; ++db) {
-              const uint32_t at0 = (stage + v_off) ^ (db * 64);
-              const uint32_t at1 = (stage + (v_off ^ 32)) ^ (db * 64);
-              const uint32_t rows = (nb * 32 + ks * 16) * (DP * 2);
-              const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                  (__attribute__((address_space(3))) s16x4*)(at0 + rows));
-              const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                  (__attribute__((address_space(3))) s16x4*)(at1 + rows + 8 * (DP * 2)));
-              const s16x8 vf = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
-              acc[db] = E::mfma(vf, pf, acc[db]);
-            }
-          }
+          for (int i = 0; i < STEP / 2; ++i)
+            acc[db0 + i] = E::mfma(vf[st % 2][i], pf, acc[db0 + i]);
         }
       }
     }
