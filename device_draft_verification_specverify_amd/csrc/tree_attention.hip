@@ -71,9 +71,17 @@ struct AttnArgs {
   int Hq, Hkv, G, D, max_nodes, words, page_shift;
   float scale_log2;
   // workspace
-  int64_t* first_tile;  // [B + 1] tiles in front of each request
-  float* part;          // [workers * 2][M][DP + 2]: sums, then m and l
+  struct Split* split;  // [workers], and all tiles in one more's start
+  float* part;          // [workers * 2][M][DP + 4]: sums, then m and l
   int tile_keys, tile_rows, width;
+};
+
+// An item (request, key head, row tile) that a worker began inside of: its tiles
+// count from `start` in the order of all tiles.
+struct Split {
+  int64_t start, first;  // first: the request's first row
+  int32_t tiles;         // 0: none
+  int32_t h, row0, rows; // rows of the item, from row0 on, of `rows` in all
 };
 
 __device__ const u32x4 zero_piece = {0, 0, 0, 0};
@@ -83,19 +91,53 @@ struct Req {
   int64_t first;
   int32_t n, len, tiles, row_tiles;
 };
-__device__ __forceinline__ Req request(const AttnArgs& a, int64_t b) {
+__device__ __forceinline__ Req request(const AttnArgs& a, int64_t b, int* bits = nullptr) {
   Req r;
   const Nodes nd = nodes_of(a.node_start, b, a.T, a.max_nodes);
   r.first = nd.first;
   r.n = nd.n < 0 ? 0 : nd.n;
   const int64_t len = a.prefix_len[b];
   r.len = int32_t(len < 0 ? 0 : len > a.max_keys ? a.max_keys : len);
+  if (bits) *bits |= (nd.n < 0 ? SV_ERR_TREE : 0) | (r.len != len ? SV_ERR_LENGTH : 0);
   r.tiles = (r.len + r.n + a.tile_keys - 1) / a.tile_keys;
   r.row_tiles = (r.n * a.G + a.tile_rows - 1) / a.tile_rows;
   return r;
 }
-__device__ __forceinline__ int64_t tiles_of(const AttnArgs& a, const Req& r) {
-  return int64_t(r.tiles) * r.row_tiles * a.Hkv;
+// The kernel's arguments where they are seldom used: read again at each such
+// place, or some hundred of them would be held in scalar registers throughout
+// and push out what the loop over the tiles uses.
+typedef const __attribute__((address_space(4))) AttnArgs* Args;
+__device__ __forceinline__ Args seldom() {
+  Args p = (Args)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return p;
+}
+
+// The same for an index that the whole workgroup has: by scalar loads.
+template <typename T>
+__device__ __forceinline__ const __attribute__((address_space(4))) T* constant(const T* p) {
+  return reinterpret_cast<const __attribute__((address_space(4))) T*>(
+      reinterpret_cast<uintptr_t>(p));
+}
+__device__ __forceinline__ Req uniform_request(Args a, int64_t b) {
+  const auto* start = constant(a->node_start) + b;
+  const int64_t lo = start[0], hi = start[1], len = constant(a->prefix_len)[b];
+  const bool good = lo >= 0 && hi >= lo && hi <= a->T && hi - lo <= a->max_nodes;
+  Req r;
+  r.first = good ? lo : 0;
+  r.n = good ? int32_t(hi - lo) : 0;
+  r.len = int32_t(len < 0 ? 0 : len > a->max_keys ? a->max_keys : len);
+  r.tiles = (r.len + r.n + a->tile_keys - 1) / a->tile_keys;
+  r.row_tiles = (r.n * a->G + a->tile_rows - 1) / a->tile_rows;
+  return r;
+}
+__device__ __forceinline__ int64_t tiles_of(int heads, const Req& r) {
+  return int64_t(r.tiles) * r.row_tiles * heads;
+}
+
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  return int64_t(uint64_t(uint32_t(uniform(int(x >> 32)))) << 32 | uint32_t(uniform(int(x))));
 }
 
 // Worker w's share of `total` tiles starts here.
@@ -139,6 +181,13 @@ __device__ __forceinline__ void load_lds16(const char* from, uint32_t to) {
                : "memory", "m0");
 }
 
+__device__ __forceinline__ void load_lds4(const int32_t* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(to), "v"(from)
+               : "memory", "m0");
+}
+
 // This wavefront's loads but the newest N have landed and its LDS reads are
 // done; then the workgroup meets.
 template <int N>
@@ -148,7 +197,23 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("" : : : "memory");
 }
 
-constexpr int kTablePart = 1024;  // page ids held in LDS at a time
+__device__ __forceinline__ void meet() {
+  asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" : : : "memory");
+}
+
+// Where the fetching side stands among the items.
+struct Cursor {
+  int64_t at, end, b, b_first;  // next tile, the share's end, its request, that one's first tile
+  Req rq;
+};
+
+// A share of an item's tiles, as the fetching side hands it to the computing one.
+struct Seg {
+  int64_t start, first;
+  int32_t n, len, h, rt, t0, t1, tiles;
+};
 
 // RW wavefronts along the rows (32 each), KW along a tile's keys (KB each), a
 // ring of S tiles.
@@ -167,12 +232,18 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   static_assert(KT * CPR % NT == 0, "whole rounds of 16-byte pieces");
   constexpr int STAGE = 2 * KT * DP * 2;  // bytes of a tile's keys and values
   constexpr int LOADS = 2 * UNITS;        // of a thread for a tile
-  static_assert((KW - 1) * RW * ND * 16 * 64 * 4 <= S * STAGE, "the merge fits the tile");
+  // blocks of 32 columns that the wavefronts along the keys join at a time
+  constexpr int BOX = (KW > 1 ? KW - 1 : 1) * RW * 16 * 64 * 4;
+  constexpr int JOIN = STAGE / BOX < ND ? STAGE / BOX : ND;
+  static_assert(KW == 1 || (JOIN >= 1 && ND % JOIN == 0), "the join fits a stage");
   __shared__ __align__(1024) char tile[S * STAGE];
-  __shared__ int32_t ids[kTablePart];
   __shared__ float merge_ml[KW][RW][2][32];
-  __shared__ int64_t scan[NT / 64 + 1];
+  __shared__ int64_t scan[NT / 64];
   __shared__ int64_t found[2];
+  __shared__ Seg segs[S];
+  __shared__ Cursor cursor;
+  __shared__ int32_t id_box[NT / 64][64];
+  __shared__ int wild_seg;
   const int tid = int(threadIdx.x), lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rw = wv % RW, kw = wv / RW;
@@ -183,57 +254,66 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   const int workers = int(gridDim.x);
   const int64_t w = workers % 8 == 0 ? (blockIdx.x % 8) * (workers / 8) + blockIdx.x / 8
                                      : blockIdx.x;
-  int64_t total = 0;
-  for (int64_t o = tid; o < a.B; o += NT) total += tiles_of(a, request(a, o));
-  for (int d = 32; d >= 1; d /= 2) total += __shfl_xor(total, d);
-  if (lane == 0) scan[wv] = total;
-  __syncthreads();
-  total = 0;
-  for (int k = 0; k < NT / 64; ++k) total += scan[k];
-  __syncthreads();
-  int64_t at = share_start(total, workers, w);
-  const int64_t end = share_start(total, workers, w + 1);
-  if (at >= end && w != 0) return;
-
-  // the request that holds tile `at`; worker 0 writes down where all begin
-  int64_t base = 0;
+  if (tid == 0) {
+    a.split[w].tiles = 0;
+    wild_seg = -1;
+  }
+  // All tiles, and those in front of this thread's request (of the last round).
+  int64_t total = 0, mine = 0, lo = 0;
   for (int64_t o = 0; o < a.B; o += NT) {
-    int64_t mine = o + tid < a.B ? tiles_of(a, request(a, o + tid)) : 0;
+    int bits = 0;
+    mine = o + tid < a.B ? tiles_of(a.Hkv, request(a, o + tid, &bits)) : 0;
+    if (w == 0 && bits) set_error(a.err, bits);
     int64_t s = mine;
     for (int d = 1; d < 64; d *= 2) {
       const int64_t y = __shfl_up(s, d);
       if (lane >= d) s += y;
     }
+    if (o) __syncthreads();
     if (lane == 63) scan[wv] = s;
     __syncthreads();
-    int64_t before = base;
-    for (int k = 0; k < wv; ++k) before += scan[k];
-    int64_t all = base;
-    for (int k = 0; k < NT / 64; ++k) all += scan[k];
-    const int64_t lo = before + s - mine;
-    if (w == 0 && o + tid < a.B) a.first_tile[o + tid] = lo;
+    lo = total + s - mine;
+    for (int k = 0; k < NT / 64; ++k) {
+      if (k < wv) lo += scan[k];
+      total += scan[k];
+    }
+  }
+  int64_t at = share_start(total, workers, w);
+  const int64_t end = share_start(total, workers, w + 1);
+  if (w == 0 && tid == 0) a.split[workers].start = total;
+  if (at >= end) return;
+  // the request that holds tile `at`: more than NT of them are gone through again
+  int64_t base = 0;
+  for (int64_t o = 0; o < a.B; o += NT) {
+    if (a.B > NT) {
+      mine = o + tid < a.B ? tiles_of(a.Hkv, request(a, o + tid)) : 0;
+      int64_t s = mine;
+      for (int d = 1; d < 64; d *= 2) {
+        const int64_t y = __shfl_up(s, d);
+        if (lane >= d) s += y;
+      }
+      __syncthreads();
+      if (lane == 63) scan[wv] = s;
+      __syncthreads();
+      lo = base + s - mine;
+      for (int k = 0; k < NT / 64; ++k) {
+        if (k < wv) lo += scan[k];
+        base += scan[k];
+      }
+    }
     if (at >= lo && at < lo + mine) {
       found[0] = o + tid;
       found[1] = lo;
     }
-    base = all;
-    __syncthreads();
-    if (w != 0 && base > at) break;
+    if (base > at) break;
   }
-  if (w == 0 && tid == 0) a.first_tile[a.B] = total;
-  if (w == 0) {  // wrong requests are reported once
-    int bits = 0;
-    for (int64_t o = tid; o < a.B; o += NT) {
-      const int64_t len = a.prefix_len[o];
-      if (len < 0 || len > a.max_keys) bits |= SV_ERR_LENGTH;
-      if (nodes_of(a.node_start, o, a.T, a.max_nodes).n < 0) bits |= SV_ERR_TREE;
-    }
-    if (bits) set_error(a.err, bits);
+  __syncthreads();
+  const int64_t count = end - at;
+  if (tid == 0) {
+    const int64_t b = found[0];
+    cursor = Cursor{at, end, b, found[1], request(a, b)};
   }
-  if (at >= end) return;
-  int64_t b = found[0];
-  int64_t b_first = found[1];
-  Req rq = request(a, b);
+  __syncthreads();
 
   // This lane's places in a stage. K: row col, piece 2 ks + half; V: 4 keys from
   // 4 half on at 4 columns. Pieces are swizzled by their row, rows a multiple of
@@ -246,400 +326,505 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
                          (lane & 1) * 8;
   const uint32_t tile_at = __builtin_amdgcn_readfirstlane(
       uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)tile)));
-  while (at < end) {
-    while (at >= b_first + tiles_of(a, rq)) {
-      b_first += tiles_of(a, rq);
-      rq = request(a, ++b);
-    }
-    const int item = int((at - b_first) / rq.tiles);  // (key head, row tile)
-    const int t0 = int((at - b_first) - int64_t(item) * rq.tiles);
-    const int t1 = int(rq.tiles - t0 < end - at ? rq.tiles : t0 + (end - at));
-    const int h = item / rq.row_tiles, rt = item - h * rq.row_tiles;
-    const int n = rq.n, len = rq.len, keys = len + n;
-    const int32_t* const table = a.table + b * a.table_stride;
+  // ---- the fetching side: S - 1 tiles ahead, over the ends of items
+  int f_t = 0, f_t1 = 0, f_seg = 0, f_len = 0, f_keys = 0, f_batch = 0;
+  const char *f_head = nullptr, *f_node = nullptr;
+  const int32_t* f_table = nullptr;
+  const char* const zero = reinterpret_cast<const char*>(&zero_piece);
+  const int64_t c_page = a.c_page, c_token = a.c_token, v_cache = a.v_cache;
+  const int in_page = (1 << a.page_shift) - 1, page_shift = a.page_shift;
+  const uint32_t num_pages = uint32_t(a.num_pages);
+  const bool full = DP == a.D;
+  constexpr int WROWS = 64 / CPR;  // rows of a wavefront's load
+  // The pieces of a row come in the same order for every round of 16 rows and
+  // more, so a lane's part of the addresses is one offset.
+  constexpr bool SAME = NT / CPR % 16 == 0;
+  const int lane_row = lane / CPR;
+  // The rows of a wavefront's load lie in one page, so its page ids are UNITS a
+  // tile. A register holds those of BATCH tiles, one a lane; the next BATCH are
+  // on their way to LDS meanwhile (they have landed by then: BATCH >= S).
+  const bool one_page = (WROWS >> page_shift) <= 1;
+  constexpr int BATCH = 64 / UNITS;
+  static_assert(BATCH >= S && UNITS <= 64, "a batch of page ids lands in time");
+  int32_t ids = 0;
+  const uint32_t id_at = uniform(
+      int(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)&id_box[wv][0])));
+  // this lane's page id in the batch of tiles from t on (the prefix's last at most)
+  auto id_place = [&](int t) {
+    const int key = (t + lane / UNITS) * KT + lane % UNITS * (NT / CPR) + wv * WROWS;
+    return f_table + ((key < f_len ? key : f_len - 1) >> page_shift);
+  };
 
-    // this lane's row
-    const int r = rt * M + rw * 32 + col;
-    const bool row_ok = r < n * a.G;
-    const int node = row_ok ? r / a.G : 0;
-    const int hq = h * a.G + (row_ok ? r - node * a.G : 0);
-    const bool wave_ok = rt * M + rw * 32 < n * a.G;
-    uint64_t see0 = 0, see1 = 0;
-    typename E::vec qf[DP / 16];
-    if (wave_ok) {
-      const char* qp = a.q + (rq.first + node) * a.q_t + hq * a.q_h;
-#pragma unroll
-      for (int s = 0; s < DP / 16; ++s) {
-        const int d = 16 * s + 8 * half;
-        u32x4 x = {0, 0, 0, 0};
-        if (d < a.D) x = *reinterpret_cast<const u32x4*>(qp + d * 2);
-        qf[s] = __builtin_bit_cast(typename E::vec, x);
-      }
-      if (a.anc) {
-        const uint64_t* m = a.anc + (rq.first + node) * a.words;
-        see0 = m[0];
-        if (a.words > 1) see1 = m[1];
-      } else {
-        see0 = node >= 63 ? ~uint64_t(0) : (uint64_t(2) << node) - 1;
-        see1 = node < 64 ? 0 : node >= 127 ? ~uint64_t(0) : (uint64_t(2) << (node - 64)) - 1;
-      }
-      // bits behind the tree are none of its nodes
-      see0 &= n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1;
-      see1 &= n >= 128 ? ~uint64_t(0) : n <= 64 ? 0 : (uint64_t(1) << (n - 64)) - 1;
+  auto next_segment = [&]() {
+    const Args s = seldom();
+    meet();  // the cursor is written
+    int64_t at = uniform(cursor.at), b = uniform(cursor.b), b_first = uniform(cursor.b_first);
+    const int64_t end = uniform(cursor.end);
+    Req rq{uniform(cursor.rq.first), uniform(cursor.rq.n), uniform(cursor.rq.len),
+           uniform(cursor.rq.tiles), uniform(cursor.rq.row_tiles)};
+    while (at >= b_first + tiles_of(s->Hkv, rq)) {
+      b_first += tiles_of(s->Hkv, rq);
+      rq = uniform_request(s, ++b);
     }
-    f32x16 acc[ND];
-#pragma unroll
-    for (int i = 0; i < ND; ++i) acc[i] = f32x16{0};
-    float m = -INFINITY, l = 0.0f;
-    int wild = 0;
-
-    // Page ids of the share, a part at a time; bad ones become -1.
-    int ids_from = 0, ids_to = 0;  // pages held
-    auto fetch_ids = [&](int t) {
-      const int need = min(min(t * KT + KT, len) - 1, len - 1) >> a.page_shift;
-      if (len == 0 || t * KT >= len || need < ids_to) return;
-      __syncthreads();  // the ids before are read
-      ids_from = (t * KT) >> a.page_shift;
-      const int last = (min(t1 * KT, len) - 1) >> a.page_shift;
-      ids_to = min(ids_from + kTablePart, last + 1);
-      for (int i = tid; i < ids_to - ids_from; i += NT) {
-        int32_t id = table[ids_from + i];
-        if (id < 0 || id >= a.num_pages) {
-          set_error(a.err, SV_ERR_PAGE);
-          id = -1;
-        }
-        ids[i] = id;
+    const int64_t into = at - b_first;
+    const int item = int(into / rq.tiles);  // (key head, row tile)
+    Seg sg;
+    sg.t0 = int(into - int64_t(item) * rq.tiles);
+    sg.t1 = int(rq.tiles - sg.t0 < end - at ? rq.tiles : sg.t0 + (end - at));
+    sg.start = at - sg.t0;
+    sg.first = rq.first;
+    sg.n = rq.n;
+    sg.len = rq.len;
+    sg.h = item / rq.row_tiles;
+    sg.rt = item - sg.h * rq.row_tiles;
+    sg.tiles = rq.tiles;
+    at += sg.t1 - sg.t0;
+    meet();  // everyone has read the cursor
+    if (tid == 0) {
+      segs[f_seg % S] = sg;
+      cursor = Cursor{at, end, b, b_first, rq};
+    }
+    ++f_seg;
+    f_t = sg.t0;
+    f_t1 = sg.t1;
+    f_len = rq.len;
+    f_keys = rq.len + rq.n;
+    f_head = s->k_cache + sg.h * s->c_h;
+    f_node = s->k_tree + rq.first * s->n_t + sg.h * s->n_h;
+    f_table = s->table + b * s->table_stride;
+    f_batch = f_t;
+    if (one_page && f_len > 0) {
+      ids = *id_place(f_t);
+      if (f_t + BATCH < f_t1) load_lds4(id_place(f_t + BATCH), id_at);
+    }
+  };
+  // Starts the next tile's keys and values on their way into a stage.
+  auto fetch_next = [&](int to_stage) {
+    if (f_t == f_t1) next_segment();
+    const int t = f_t++;
+    const uint32_t stage = tile_at + uint32_t(to_stage) * STAGE + wv * 1024;
+    if (t - f_batch == BATCH) {
+      f_batch = t;
+      if (one_page && f_len > 0) {
+        ids = id_box[wv][lane];
+        asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(ids) : : "memory");
+        if (t + BATCH < f_t1) load_lds4(id_place(t + BATCH), id_at);
       }
-      __syncthreads();
-    };
-    // Starts a tile's keys and values on their way into stage t % S. Branches
-    // only where the whole workgroup takes them; lanes choose between addresses.
-    const char* const zero = reinterpret_cast<const char*>(&zero_piece);
-    const char* const k_head = a.k_cache + h * a.c_h;
-    const char* const k_node = a.k_tree + rq.first * a.n_t + h * a.n_h;
-    const int64_t c_page = a.c_page, c_token = a.c_token, v_cache = a.v_cache;
-    const int in_page = (1 << a.page_shift) - 1, page_shift = a.page_shift;
-    auto fetch = [&](int t) {
-      fetch_ids(t);
-      const uint32_t stage = tile_at + uint32_t(t % S) * STAGE;
-      const int key0 = t * KT + tid / CPR;
-      const bool inside = t * KT + KT <= len;  // cached keys only
-      int32_t id[UNITS];
+    }
+    const int id0 = (t - f_batch) * UNITS;
+    bool quick = one_page && t * KT + KT <= f_len;
+    if (quick) {
+      const bool here = lane >= id0 && lane < id0 + UNITS;
+      quick = !__any(here && uint32_t(ids) >= num_pages);
+    }
+    if (quick) {
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) {
-        const int key = key0 + u * (NT / CPR);
-        const int at_id = (key >> page_shift) - ids_from;
-        id[u] = ids[inside || key < len ? at_id : 0];
-      }
-#pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        const int row = u * (NT / CPR) + tid / CPR;
-        // rounds of 16 rows and more repeat the order of pieces
-        const int c = (tid % CPR) ^ swizzle<CPR>(NT / CPR % 16 == 0 ? tid / CPR : row);
-        const int key = t * KT + row;
-        const char* kp = k_head + c * 16 + uint32_t(id[u]) * uint64_t(c_page) +
-                         uint32_t(key & in_page) * uint64_t(c_token);
-        bool some = id[u] >= 0;
+        const int row0 = u * (NT / CPR) + wv * WROWS;
+        const int c = (lane % CPR) ^ swizzle<CPR>(SAME ? wv * WROWS + lane_row : row0 + lane_row);
+        const char* base =
+            f_head + uint32_t(__builtin_amdgcn_readlane(ids, id0 + u)) * uint64_t(c_page) +
+            uint32_t((t * KT + row0) & in_page) * uint64_t(c_token);
+        const char* kp = base + (lane_row * c_token + c * 16);
         const char* vp = kp + v_cache;
-        if (!inside) {
-          const char* np = k_node + c * 16 + int64_t(key - len) * a.n_t;
-          const char* nv = np + a.v_tree;
-          some = key < len ? some : key < keys;
-          kp = key < len ? kp : np;
-          vp = key < len ? vp : nv;
+        if (!full) {
+          const bool some = c * 8 < a.D;
+          kp = some ? kp : zero;
+          vp = some ? vp : zero;
         }
-        some = some && (DP == a.D || c * 8 < a.D);
-        kp = some ? kp : zero;
-        vp = some ? vp : zero;
-        const uint32_t to = stage + (u * NT + wv * 64) * 16;
-        load_lds16(kp, to);
-        load_lds16(vp, to + KT * DP * 2);
+        load_lds16(kp, stage + u * NT * 16);
+        load_lds16(vp, stage + u * NT * 16 + KT * DP * 2);
       }
-    };
+    } else {
+      // the end of the prefix, the tree's nodes, pages of fewer rows than a
+      // wavefront loads, bad pages: lane by lane
+      const Args s = seldom();
+      int32_t page[UNITS];
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i)
-      if (t0 + i < t1) fetch(t0 + i);
+      for (int u = 0; u < UNITS; ++u) {
+        const int key = t * KT + u * (NT / CPR) + wv * WROWS + lane_row;
+        page[u] = -1;
+        if (one_page) page[u] = __builtin_amdgcn_readlane(ids, id0 + u);
+        else if (f_len > 0) page[u] = f_table[(key < f_len ? key : f_len - 1) >> page_shift];
+      }
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        const int row = u * (NT / CPR) + wv * WROWS + lane_row;
+        const int c = (lane % CPR) ^ swizzle<CPR>(row);
+        const int key = t * KT + row;
+        const char* cp = f_head + uint32_t(page[u]) * uint64_t(c_page) +
+                         uint32_t(key & in_page) * uint64_t(c_token);
+        const char* np = f_node + int64_t(key - f_len) * s->n_t;
+        const bool cached = key < f_len, good = uint32_t(page[u]) < num_pages;
+        const bool some = c * 8 < s->D && (cached ? good : key < f_keys);
+        if (cached && !good) set_error(s->err, SV_ERR_PAGE);
+        const char* kp = (cached ? cp : np) + c * 16;
+        const char* vp = kp + (cached ? v_cache : s->v_tree);
+        load_lds16(some ? kp : zero, stage + u * NT * 16);
+        load_lds16(some ? vp : zero, stage + u * NT * 16 + KT * DP * 2);
+      }
+    }
+  };
 
-    for (int t = t0; t < t1; ++t) {
-      // tile t is here; everyone is done with tile t - 1, whose stage is next
-      if (S >= 4 && t1 - t > 2) wait_and_meet<2 * LOADS>();
-      else if (S >= 3 && t1 - t > 1) wait_and_meet<LOADS>();
-      else wait_and_meet<0>();
-      if (t + S - 1 < t1) fetch(t + S - 1);
-      char* const tv = tile + (t % S) * STAGE + KT * DP * 2;
-      const uint32_t stage = tile_at + uint32_t(t % S) * STAGE;
-      // Nodes' values that are infinite or NaN would reach the rows that do not
-      // see them as 0 * inf: they become zeros here and are added at the end.
-      if (t * KT + KT > len) {
-        bool mine = false;
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          const int unit = u * NT + tid;
-          const int key = t * KT + unit / CPR;
-          if (key >= len && key < keys) {
-            u32x4* at16 = reinterpret_cast<u32x4*>(tv + unit * 16);
-            u32x4 x = *at16;
-            bool any = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t lo = E::wild(x[i]) ? 0xFFFFu : 0, hi = E::wild(x[i] >> 16) ? ~0xFFFFu : 0;
-              any = any || lo || hi;
-              x[i] &= ~(lo | hi);
-            }
-            if (any) *at16 = x;
-            mine = mine || any;
-          }
-        }
-        wild |= __syncthreads_or(mine);
-      }
+  // ---- the computing side
+  int t = 0, t1 = 0, seg = 0;
+  int len = 0, n = 0, keys = 0;
+  int hq = 0, node = 0, wild = 0;
+  bool row_ok = false, wave_ok = false;
+  uint64_t see0 = 0, see1 = 0;
+  typename E::vec qf[DP / 16];
+  f32x16 acc[ND];
+  float m = -INFINITY, l = 0.0f;
+
+#pragma unroll 1
+  for (int i = 0; i < S - 1; ++i)
+    if (i < count) fetch_next(i);
+  int st_now = 0, st_next = S - 1;  // stages of this tile and of the one to fetch
+  for (int64_t left = count; left > 0; --left) {
+    // this tile is here; everyone is done with the one before, whose stage is next
+    if (S >= 4 && left > 2) wait_and_meet<2 * LOADS>();
+    else if (S >= 3 && left > 1) wait_and_meet<LOADS>();
+    else wait_and_meet<0>();
+
+    if (t == t1) {
+      const Args s = seldom();
+      const Seg& sg = segs[seg % S];
+      t = uniform(sg.t0);
+      t1 = uniform(sg.t1);
+      len = uniform(sg.len);
+      n = uniform(sg.n);
+      const int h = uniform(sg.h), rt = uniform(sg.rt);
+      const int64_t first = uniform(sg.first);
+      keys = len + n;
+      ++seg;
+      const int r = rt * M + rw * 32 + col;
+      row_ok = r < n * s->G;
+      node = row_ok ? r / s->G : 0;
+      hq = h * s->G + (row_ok ? r - node * s->G : 0);
+      wave_ok = rt * M + rw * 32 < n * s->G;
+      see0 = see1 = 0;
       if (wave_ok) {
-        // Fragments are read ahead of the products that take them, 8 at a time
-        // (the barriers keep the compiler from pulling each read down to its
-        // use, where its latency would show).
-        f32x16 s[NB];
+        const char* qp = s->q + (first + node) * s->q_t + hq * s->q_h;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          s[nb] = f32x16{0};
+        for (int k = 0; k < DP / 16; ++k) {
+          const int d = 16 * k + 8 * half;
+          u32x4 x = {0, 0, 0, 0};
+          if (d < s->D) x = *reinterpret_cast<const u32x4*>(qp + d * 2);
+          qf[k] = __builtin_bit_cast(typename E::vec, x);
+        }
+        if (s->anc) {
+          const uint64_t* words = s->anc + (first + node) * s->words;
+          see0 = words[0];
+          if (s->words > 1) see1 = words[1];
+        } else {
+          see0 = node >= 63 ? ~uint64_t(0) : (uint64_t(2) << node) - 1;
+          see1 = node < 64 ? 0 : node >= 127 ? ~uint64_t(0) : (uint64_t(2) << (node - 64)) - 1;
+        }
+        // bits behind the tree are none of its nodes
+        see0 &= n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1;
+        see1 &= n >= 128 ? ~uint64_t(0) : n <= 64 ? 0 : (uint64_t(1) << (n - 64)) - 1;
+      }
 #pragma unroll
-          for (int k8 = 0; k8 < DP / 16; k8 += STEP) {
-            s16x8 kf[STEP];
+      for (int i = 0; i < ND; ++i) acc[i] = f32x16{0};
+      m = -INFINITY;
+      l = 0.0f;
+      wild = 0;
+      // the rows have to come before further tiles queue in front of them
+      asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    }
+    if (left > S - 1) fetch_next(st_next);
+    char* const tv = tile + st_now * STAGE + KT * DP * 2;
+    const uint32_t stage = tile_at + uint32_t(st_now) * STAGE;
+    // Nodes' values that are infinite or NaN would reach the rows that do not
+    // see them as 0 * inf: they become zeros here and are added at the end.
+    if (t * KT + KT > len) {
+      bool mine = false;
 #pragma unroll
-            for (int i = 0; i < STEP; ++i)
-              kf[i] = *reinterpret_cast<__attribute__((address_space(3))) const s16x8*>(
-                  ((stage + k_off) ^ ((k8 + i) * 32)) + nb * 32 * (DP * 2));
-            __builtin_amdgcn_sched_barrier(0);
+      for (int u = 0; u < UNITS; ++u) {
+        const int unit = u * NT + tid;
+        const int key = t * KT + unit / CPR;
+        if (key >= len && key < keys) {
+          u32x4* at16 = reinterpret_cast<u32x4*>(tv + unit * 16);
+          u32x4 x = *at16;
+          bool any = false;
 #pragma unroll
-            for (int i = 0; i < STEP; ++i) s[nb] = E::mfma(kf[i], qf[k8 + i], s[nb]);
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = E::wild(x[i]) ? 0xFFFFu : 0, hi = E::wild(x[i] >> 16) ? ~0xFFFFu : 0;
+            any = any || lo || hi;
+            x[i] &= ~(lo | hi);
           }
+          if (any) *at16 = x;
+          mine = mine || any;
         }
-        // V^T of a half block of keys: columns d of this lane, keys in the order
-        // of the scores
-        s16x8 vf[2][STEP / 2];
-        auto read_v = [&](int half_block, int db0, s16x8* to) {
+      }
+      if (mine) wild_seg = seg;
+      meet();
+      wild = wild_seg == seg;
+    }
+    if (wave_ok) {
+      // Fragments are read ahead of the products that take them, 8 at a time
+      // (the barriers keep the compiler from pulling each read down to its
+      // use, where its latency would show).
+      f32x16 s[NB];
 #pragma unroll
-          for (int i = 0; i < STEP / 2; ++i) {
-            const uint32_t at = (stage + v_off) ^ ((db0 + i) * 64);
-            const uint32_t rows = half_block * 16 * (DP * 2);
-            const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)(at + rows));
-            const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4*)((at ^ 32) + rows + 8 * (DP * 2)));
-            to[i] = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
-          }
-        };
-        read_v(0, 0, vf[0]);
-        __builtin_amdgcn_sched_barrier(0);
-        const int key0 = t * KT + kw * KB + 4 * half;
-        if (t * KT + KT > len) {
-          const uint64_t see = window(see0, see1, key0 - len);
+      for (int nb = 0; nb < NB; ++nb) {
+        s[nb] = f32x16{0};
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+        for (int k8 = 0; k8 < DP / 16; k8 += STEP) {
+          s16x8 kf[STEP];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint32_t bit = uint32_t(see >> (nb * 32)) & (1u << (8 * (i / 4) + i % 4));
-              s[nb][i] = bit ? s[nb][i] : -INFINITY;
-            }
+          for (int i = 0; i < STEP; ++i)
+            kf[i] = *reinterpret_cast<__attribute__((address_space(3))) const s16x8*>(
+                ((stage + k_off) ^ ((k8 + i) * 32)) + nb * 32 * (DP * 2));
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int i = 0; i < STEP; ++i) s[nb] = E::mfma(kf[i], qf[k8 + i], s[nb]);
         }
-        float top = -INFINITY;
+      }
+      // V^T of a half block of keys: columns d of this lane, keys in the order
+      // of the scores
+      s16x8 vf[2][STEP / 2];
+      auto read_v = [&](int half_block, int db0, s16x8* to) {
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) top = fmaxf(top, s[nb][i]);
-        top *= a.scale_log2;
-        top = fmaxf(top, __shfl_xor(top, 32));
-        if (__any(top > m)) {
-          const float to = fmaxf(m, top);
-          const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-          l *= f;
-#pragma unroll
-          for (int i = 0; i < ND; ++i) acc[i] *= f;
-          m = to;
+        for (int i = 0; i < STEP / 2; ++i) {
+          const uint32_t at = (stage + v_off) ^ ((db0 + i) * 64);
+          const uint32_t rows = half_block * 16 * (DP * 2);
+          const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s16x4*)(at + rows));
+          const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s16x4*)((at ^ 32) + rows + 8 * (DP * 2)));
+          to[i] = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
         }
-        const float ref = m == -INFINITY ? 0.0f : m;
+      };
+      read_v(0, 0, vf[0]);
+      __builtin_amdgcn_sched_barrier(0);
+      const int key0 = t * KT + kw * KB + 4 * half;
+      if (t * KT + KT > len) {
+        const uint64_t see = window(see0, see1, key0 - len);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            s[nb][i] = __builtin_amdgcn_exp2f(fmaf(s[nb][i], a.scale_log2, -ref));
-            l += s[nb][i];
+            const uint32_t bit = uint32_t(see >> (nb * 32)) & (1u << (8 * (i / 4) + i % 4));
+            s[nb][i] = bit ? s[nb][i] : -INFINITY;
           }
-        // V is read one step (a half block of keys, STEP / 2 blocks of columns)
-        // ahead of its products
-        constexpr int PER = ND / (STEP / 2), STEPS = 2 * NB * PER;
-#pragma unroll
-        for (int st = 0; st < STEPS; ++st) {
-          const int hb = st / PER, db0 = st % PER * (STEP / 2);
-          if (st + 1 < STEPS) read_v((st + 1) / PER, (st + 1) % PER * (STEP / 2), vf[(st + 1) % 2]);
-          typename E::vec pf;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) pf[j] = elem(s[hb / 2][8 * (hb % 2) + j]);
-          __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-          for (int i = 0; i < STEP / 2; ++i)
-            acc[db0 + i] = E::mfma(vf[st % 2][i], pf, acc[db0 + i]);
-        }
       }
-    }
-    __syncthreads();
-    l += __shfl_xor(l, 32);
-
-    if constexpr (KW > 1) {
-      // the wavefronts along the keys join in LDS
-      if (half == 0) {
-        merge_ml[kw][rw][0][col] = m;
-        merge_ml[kw][rw][1][col] = l;
-      }
-      float* const box = reinterpret_cast<float*>(tile);
-      if (kw > 0) {
-        float* o = box + ((kw - 1) * RW + rw) * (ND * 16 * 64);
+      float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < ND; ++i)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[(i * 16 + j) * 64 + lane] = acc[i][j];
-      }
-      __syncthreads();
-      if (kw == 0) {
-        float to = m;
-#pragma unroll
-        for (int k = 1; k < KW; ++k) to = fmaxf(to, merge_ml[k][rw][0][col]);
-        const float ref = to == -INFINITY ? 0.0f : to;
-        float f = __builtin_amdgcn_exp2f(m - ref);
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[nb][i]);
+      top *= a.scale_log2;
+      top = fmaxf(top, __shfl_xor(top, 32));
+      if (__any(top > m)) {
+        const float to = fmaxf(m, top);
+        const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
         l *= f;
 #pragma unroll
         for (int i = 0; i < ND; ++i) acc[i] *= f;
+        m = to;
+      }
+      const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-        for (int k = 1; k < KW; ++k) {
-          f = __builtin_amdgcn_exp2f(merge_ml[k][rw][0][col] - ref);
-          l += f * merge_ml[k][rw][1][col];
-          const float* o = box + ((k - 1) * RW + rw) * (ND * 16 * 64);
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          s[nb][i] = __builtin_amdgcn_exp2f(fmaf(s[nb][i], a.scale_log2, -ref));
+          l += s[nb][i];
+        }
+      // V is read one step (a half block of keys, STEP / 2 blocks of columns)
+      // ahead of its products
+      constexpr int PER = ND / (STEP / 2), STEPS = 2 * NB * PER;
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st) {
+        const int hb = st / PER, db0 = st % PER * (STEP / 2);
+        if (st + 1 < STEPS) read_v((st + 1) / PER, (st + 1) % PER * (STEP / 2), vf[(st + 1) % 2]);
+        typename E::vec pf;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) pf[j] = elem(s[hb / 2][8 * (hb % 2) + j]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < STEP / 2; ++i)
+          acc[db0 + i] = E::mfma(vf[st % 2][i], pf, acc[db0 + i]);
+      }
+    }
+    ++t;
+    if (t == t1) {
+      const Args s = seldom();
+      const Seg& sg = segs[(seg - 1) % S];
+      const int t0 = uniform(sg.t0), h = uniform(sg.h);
+      const int64_t first = uniform(sg.first);
+      const bool whole = t0 == 0 && t1 == uniform(sg.tiles);
+      l += __shfl_xor(l, 32);
+
+      if constexpr (KW > 1) {
+        // The wavefronts along the keys join in this tile's stage, JOIN blocks of
+        // columns at a time; the other stages are being filled.
+        if (half == 0) {
+          merge_ml[kw][rw][0][col] = m;
+          merge_ml[kw][rw][1][col] = l;
+        }
+        float* const box = reinterpret_cast<float*>(tile + st_now * STAGE);
+        float ref = 0.0f, f[KW];
+#pragma unroll
+        for (int i0 = 0; i0 < ND; i0 += JOIN) {
+          meet();
+          if (kw > 0) {
+            float* o = box + ((kw - 1) * RW + rw) * (JOIN * 16 * 64);
+#pragma unroll
+            for (int i = 0; i < JOIN; ++i)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[(i * 16 + j) * 64 + lane] = acc[i0 + i][j];
+          }
+          meet();
+          if (kw == 0) {
+            if (i0 == 0) {
+              float to = m;
+#pragma unroll
+              for (int k = 1; k < KW; ++k) to = fmaxf(to, merge_ml[k][rw][0][col]);
+              ref = to == -INFINITY ? 0.0f : to;
+              f[0] = __builtin_amdgcn_exp2f(m - ref);
+              l *= f[0];
+#pragma unroll
+              for (int k = 1; k < KW; ++k) {
+                f[k] = __builtin_amdgcn_exp2f(merge_ml[k][rw][0][col] - ref);
+                l += f[k] * merge_ml[k][rw][1][col];
+              }
+              m = to;
+            }
+#pragma unroll
+            for (int i = 0; i < JOIN; ++i) {
+              acc[i0 + i] *= f[0];
+#pragma unroll
+              for (int k = 1; k < KW; ++k) {
+                const float* o = box + ((k - 1) * RW + rw) * (JOIN * 16 * 64);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  acc[i0 + i][j] = fmaf(f[k], o[(i * 16 + j) * 64 + lane], acc[i0 + i][j]);
+              }
+              __builtin_amdgcn_sched_barrier(0);  // few registers rather than many reads at once
+            }
+          }
+        }
+      }
+
+      if (wild && kw == 0) {
+        // The wild values of the nodes among this share's keys, for the rows that
+        // see them (rare, so scores are simply taken again).
+        for (int x = max(t0 * KT - len, 0); x < min(t1 * KT - len, n); ++x) {
+          const bool see = row_ok && ((x < 64 ? see0 >> (x & 63) : see1 >> (x & 63)) & 1);
+          const char* kp = s->k_tree + (first + x) * s->n_t + h * s->n_h;
+          const elem* kx = reinterpret_cast<const elem*>(kp);
+          const elem* qx =
+              reinterpret_cast<const elem*>(s->q + (first + node) * s->q_t + hq * s->q_h);
+          const uint16_t* vx = reinterpret_cast<const uint16_t*>(kp + s->v_tree);
+          float dot = 0.0f;
+#pragma unroll 1
+          for (int d = 0; d < s->D; ++d) dot = fmaf(float(qx[d]), float(kx[d]), dot);
+          // a weight that underflows is still one
+          const float px = fmaxf(__builtin_amdgcn_exp2f(fmaf(dot, s->scale_log2, -m)), 1e-30f);
 #pragma unroll
           for (int i = 0; i < ND; ++i)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) acc[i][j] = fmaf(f, o[(i * 16 + j) * 64 + lane], acc[i][j]);
-        }
-        m = to;
-      }
-      __syncthreads();
-    }
-
-    if (wild && kw == 0) {
-      // The wild values of the nodes among this share's keys, for the rows that
-      // see them (rare, so scores are simply taken again).
-      for (int x = max(t0 * KT - len, 0); x < min(t1 * KT - len, n); ++x) {
-        const bool see = row_ok && ((x < 64 ? see0 >> (x & 63) : see1 >> (x & 63)) & 1);
-        const char* kp = a.k_tree + (rq.first + x) * a.n_t + h * a.n_h;
-        const elem* kx = reinterpret_cast<const elem*>(kp);
-        const elem* qx = reinterpret_cast<const elem*>(a.q + (rq.first + node) * a.q_t + hq * a.q_h);
-        const uint16_t* vx = reinterpret_cast<const uint16_t*>(kp + a.v_tree);
-        float dot = 0.0f;
-#pragma unroll 1
-        for (int d = 0; d < a.D; ++d) dot = fmaf(float(qx[d]), float(kx[d]), dot);
-        // a weight that underflows is still one
-        const float px = fmaxf(__builtin_amdgcn_exp2f(fmaf(dot, a.scale_log2, -m)), 1e-30f);
-#pragma unroll
-        for (int i = 0; i < ND; ++i)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int d = i * 32 + 8 * (j / 4) + 4 * half + j % 4;
-            const uint16_t raw = d < a.D ? vx[d] : 0;
-            const float sum = fmaf(px, float(__builtin_bit_cast(elem, raw)), acc[i][j]);
-            acc[i][j] = see & E::wild(raw) ? sum : acc[i][j];
-            __builtin_amdgcn_sched_barrier(0);  // few registers rather than many loads at once
-          }
-      }
-    }
-
-    if (kw == 0 && row_ok) {
-      if (t0 == 0 && t1 == rq.tiles) {
-        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-        char* op = a.out + (rq.first + node) * a.o_t + hq * a.o_h;
-#pragma unroll
-        for (int i = 0; i < ND; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int d = i * 32 + 8 * j + 4 * half;
-            if (d < a.D) {
-              typedef elem e4 __attribute__((ext_vector_type(4)));
-              e4 x;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) x[k] = elem(acc[i][4 * j + k] * inv);
-              *reinterpret_cast<e4*>(op + d * 2) = x;
+            for (int j = 0; j < 16; ++j) {
+              const int d = i * 32 + 8 * (j / 4) + 4 * half + j % 4;
+              const uint16_t raw = d < s->D ? vx[d] : 0;
+              const float sum = fmaf(px, float(__builtin_bit_cast(elem, raw)), acc[i][j]);
+              acc[i][j] = (see & E::wild(raw)) ? sum : acc[i][j];
+              __builtin_amdgcn_sched_barrier(0);  // few registers rather than many loads at once
             }
-          }
-        if (a.lse && half == 0)
-          a.lse[(rq.first + node) * a.Hq + hq] =
-              l > 0.0f || l != l ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
-      } else {
-        // a share of the keys: slot 0 of the worker if it began inside the
-        // item (its first), slot 1 if it ends inside (its last)
-        float* p = a.part + ((w * 2 + (t0 > 0 ? 0 : 1)) * M + rw * 32 + col) * int64_t(DP + 2);
-#pragma unroll
-        for (int i = 0; i < ND; ++i)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) p[i * 32 + 8 * (j / 4) + 4 * half + j % 4] = acc[i][j];
-        if (half == 0) {
-          p[DP] = m;
-          p[DP + 1] = l;
         }
       }
+
+      if (kw == 0 && row_ok) {
+        if (whole) {
+          const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+          char* op = s->out + (first + node) * s->o_t + hq * s->o_h;
+#pragma unroll
+          for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int d = i * 32 + 8 * j + 4 * half;
+              if (d < s->D) {
+                typedef elem e4 __attribute__((ext_vector_type(4)));
+                e4 x;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[k] = elem(acc[i][4 * j + k] * inv);
+                *reinterpret_cast<e4*>(op + d * 2) = x;
+              }
+            }
+          if (s->lse && half == 0)
+            s->lse[(first + node) * s->Hq + hq] =
+                l > 0.0f || l != l ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+        } else {
+          // a share of the keys: slot 0 of the worker if it began inside the
+          // item (its first), slot 1 if it ends inside (its last)
+          float* p = s->part + ((w * 2 + (t0 > 0 ? 0 : 1)) * M + rw * 32 + col) * int64_t(DP + 4);
+#pragma unroll
+          for (int i = 0; i < ND; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<f32x4*>(p + i * 32 + 8 * j + 4 * half) =
+                  f32x4{acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]};
+          if (half == 0) {
+            p[DP] = m;
+            p[DP + 1] = l;
+          }
+        }
+      }
+      if (t0 > 0 && tid == 0)
+        s->split[w] = Split{sg.start, first, sg.tiles, h, sg.rt * M, n * s->G};
     }
-    // Loads are counted in order among themselves only: no store stays behind.
-    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
-    at += t1 - t0;
+    st_now = st_now + 1 == S ? 0 : st_now + 1;
+    st_next = st_next + 1 == S ? 0 : st_next + 1;
   }
 }
 
-// Joins the shares of items that several workers had: a wavefront per row
-// (node, query head); rows of whole items end at once.
-template <int DT>
+// Joins the shares of items that several workers had. The worker that comes
+// second in an item stands for it; blockIdx.y counts groups of its rows. DP / 4
+// lanes take a row.
+template <int DT, int DP>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int workers) {
   using elem = typename Elem<DT>::type;
-  const int lane = int(threadIdx.x) & 63;
-  const int64_t row = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (row >= a.T * a.Hq) return;
-  const int64_t i = row / a.Hq;
-  const int hq = int(row - i * a.Hq);
-  // the request of row i (node_start ascends where it is right)
-  int64_t lo = 0, hi = a.B;
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) / 2;
-    if (a.node_start[mid] <= i) lo = mid;
-    else hi = mid;
-  }
-  const Req rq = request(a, lo);
-  if (i < rq.first || i >= rq.first + rq.n) return;
-  const int64_t total = a.first_tile[a.B];
-  const int h = hq / a.G;
-  const int r = int(i - rq.first) * a.G + hq - h * a.G;
-  const int rt = r / a.tile_rows;
-  const int64_t t0 = a.first_tile[lo] + (int64_t(h) * rq.row_tiles + rt) * rq.tiles;
-  const int64_t w0 = worker_of(total, workers, t0);
-  const int64_t w1 = worker_of(total, workers, t0 + rq.tiles - 1);
-  if (w0 == w1) return;
-  const int64_t step = int64_t(a.tile_rows) * (a.width + 2);
-  const float* p = a.part + int64_t(r % a.tile_rows) * (a.width + 2);
-  // w0's share is its last segment when it starts in front of the item or at it
-  auto at = [&](int64_t w) { return p + (w * 2 + (w == w0 ? 1 : 0)) * step; };
-  float m = -INFINITY;
-  for (int64_t w = w0 + lane; w <= w1; w += 64) m = fmaxf(m, at(w)[a.width]);
-  for (int d = 32; d >= 1; d /= 2) m = fmaxf(m, __shfl_xor(m, d));
-  const float ref = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f, x[4] = {0, 0, 0, 0};
-  const int d0 = lane * 4;
+  constexpr int LANES = DP / 4, ROWS = 256 / LANES;
+  const int64_t second = blockIdx.x;
+  const Split sp = a.split[second];
+  if (sp.tiles == 0) return;
+  const int r = sp.row0 + int(blockIdx.y) * ROWS + int(threadIdx.x) / LANES;
+  if (r >= sp.rows) return;
+  const int64_t total = a.split[workers].start;
+  const int64_t w0 = worker_of(total, workers, sp.start);
+  if (w0 + 1 != second) return;
+  const int64_t w1 = worker_of(total, workers, sp.start + sp.tiles - 1);
+  const int64_t step = int64_t(a.tile_rows) * (DP + 4);
+  const float* p = a.part + int64_t(r - sp.row0) * (DP + 4);
+  const int d0 = int(threadIdx.x) % LANES * 4;
+  // w0's share is its last segment, the others' their first
+  float m = -INFINITY, l = 0.0f;
+  f32x4 x = {0, 0, 0, 0};
   for (int64_t w = w0; w <= w1; ++w) {
-    const float* o = at(w);
-    const float f = __builtin_amdgcn_exp2f(o[a.width] - ref);
-    l = fmaf(f, o[a.width + 1], l);
-    if (d0 < a.D)
-      for (int k = 0; k < 4; ++k) x[k] = fmaf(f, o[d0 + k], x[k]);
+    const float* o = p + (w * 2 + (w == w0 ? 1 : 0)) * step;
+    const f32x4 y = *reinterpret_cast<const f32x4*>(o + d0);
+    const float mw = o[DP], lw = o[DP + 1];
+    const float to = fmaxf(m, mw), ref = to == -INFINITY ? 0.0f : to;
+    const float f = __builtin_amdgcn_exp2f(m - ref), g = __builtin_amdgcn_exp2f(mw - ref);
+    l = l * f + lw * g;
+    x = x * f + y * g;
+    m = to;
   }
+  const int node = r / a.G;
+  const int hq = sp.h * a.G + r - node * a.G;
   const bool some = l > 0.0f || l != l;
   const float inv = some ? 1.0f / l : 0.0f;
   if (d0 < a.D) {
-    elem* op = reinterpret_cast<elem*>(a.out + i * a.o_t + hq * a.o_h);
-    for (int k = 0; k < 4; ++k) op[d0 + k] = elem(x[k] * inv);
+    typedef elem e4 __attribute__((ext_vector_type(4)));
+    e4 y;
+    for (int k = 0; k < 4; ++k) y[k] = elem(x[k] * inv);
+    *reinterpret_cast<e4*>(a.out + (sp.first + node) * a.o_t + hq * a.o_h + d0 * 2) = y;
   }
-  if (a.lse && lane == 0) a.lse[row] = some ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+  if (a.lse && d0 == 0)
+    a.lse[(sp.first + node) * a.Hq + hq] =
+        some ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
 }
 
 // Which kernel: rows of the largest tree in wavefronts of 32 rows, and the rest
@@ -685,12 +870,17 @@ void launch(const Variant& v, const AttnArgs& a, hipStream_t st) {
 
 template <int DT>
 void launch_width(const Variant& v, const AttnArgs& a, hipStream_t st) {
-  if (v.width == 64) launch<DT, 64>(v, a, st);
-  else if (v.width == 128) launch<DT, 128>(v, a, st);
-  else launch<DT, 256>(v, a, st);
-  const int64_t rows = a.T * a.Hq;
-  hipLaunchKernelGGL((join_kernel<DT>), dim3(unsigned((rows + 3) / 4)), dim3(256), 0, st, a,
-                     v.workers);
+  const dim3 grid{unsigned(v.workers), unsigned(32 * v.rw * v.width / 1024)};
+  if (v.width == 64) {
+    launch<DT, 64>(v, a, st);
+    hipLaunchKernelGGL((join_kernel<DT, 64>), grid, dim3(256), 0, st, a, v.workers);
+  } else if (v.width == 128) {
+    launch<DT, 128>(v, a, st);
+    hipLaunchKernelGGL((join_kernel<DT, 128>), grid, dim3(256), 0, st, a, v.workers);
+  } else {
+    launch<DT, 256>(v, a, st);
+    hipLaunchKernelGGL((join_kernel<DT, 256>), grid, dim3(256), 0, st, a, v.workers);
+  }
 }
 
 bool sizes_ok(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_nodes) {
@@ -709,8 +899,8 @@ size_t specverify_tree_attention_workspace_size(int64_t B, int64_t T, int64_t Hq
                                                 int64_t D, int64_t max_nodes) {
   if (!sizes_ok(B, T, Hq, Hkv, D, max_nodes)) return 0;
   const Variant v = variant_of(max_nodes * (Hq / Hkv), D);
-  return align256(size_t(B + 1) * 8) +
-         align256(size_t(v.workers) * 2 * (32 * v.rw) * (v.width + 2) * sizeof(float));
+  return align256(size_t(v.workers + 1) * sizeof(Split)) +
+         align256(size_t(v.workers) * 2 * (32 * v.rw) * (v.width + 4) * sizeof(float));
 }
 
 int specverify_tree_attention(
@@ -783,8 +973,9 @@ int specverify_tree_attention(
   a.words = int((max_nodes + 63) / 64);
   a.page_shift = log2_of(page_size);
   a.scale_log2 = scale * kLog2e;
-  a.first_tile = static_cast<int64_t*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(size_t(B + 1) * 8));
+  a.split = static_cast<Split*>(workspace);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                    align256(size_t(v.workers + 1) * sizeof(Split)));
   a.tile_keys = v.kw * v.kb;
   a.tile_rows = 32 * v.rw;
   a.width = v.width;
