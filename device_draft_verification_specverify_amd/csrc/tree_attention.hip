@@ -131,8 +131,12 @@ __device__ __forceinline__ Req uniform_request(Args a, int64_t b) {
   r.row_tiles = (r.n * a->G + a->tile_rows - 1) / a->tile_rows;
   return r;
 }
-__device__ __forceinline__ int64_t tiles_of(int heads, const Req& r) {
-  return int64_t(r.tiles) * r.row_tiles * heads;
+// Work is shared out in places: an item (request, key head, row tile) takes one
+// for each of its tiles and kItemPlaces more for what it costs besides (rows
+// loaded, wavefronts joined, results written).
+constexpr int kItemPlaces = 3;
+__device__ __forceinline__ int64_t places_of(int heads, const Req& r) {
+  return int64_t(r.tiles + kItemPlaces) * r.row_tiles * heads;
 }
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -205,13 +209,14 @@ __device__ __forceinline__ void meet() {
 
 // Where the fetching side stands among the items.
 struct Cursor {
-  int64_t at, end, b, b_first;  // next tile, the share's end, its request, that one's first tile
+  int64_t at, b, b_first;  // the next place, its request, that one's first place
   Req rq;
 };
 
-// A share of an item's tiles, as the fetching side hands it to the computing one.
+// A share of an item's tiles, prepared while the one before is fetched.
 struct Seg {
   int64_t start, first;
+  int64_t head, node, table;  // the request's keys of this head, its nodes', its pages
   int32_t n, len, h, rt, t0, t1, tiles;
 };
 
@@ -240,9 +245,9 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   __shared__ float merge_ml[KW][RW][2][32];
   __shared__ int64_t scan[NT / 64];
   __shared__ int64_t found[2];
-  __shared__ Seg segs[S];
-  __shared__ Cursor cursor;
-  __shared__ int32_t id_box[NT / 64][64];
+  __shared__ Seg segs[S + 2];
+  __shared__ Cursor cursors[2];
+  __shared__ int32_t id_box[NT / 64][2][64];
   __shared__ int wild_seg;
   const int tid = int(threadIdx.x), lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -262,7 +267,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   int64_t total = 0, mine = 0, lo = 0;
   for (int64_t o = 0; o < a.B; o += NT) {
     int bits = 0;
-    mine = o + tid < a.B ? tiles_of(a.Hkv, request(a, o + tid, &bits)) : 0;
+    mine = o + tid < a.B ? places_of(a.Hkv, request(a, o + tid, &bits)) : 0;
     if (w == 0 && bits) set_error(a.err, bits);
     int64_t s = mine;
     for (int d = 1; d < 64; d *= 2) {
@@ -286,7 +291,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   int64_t base = 0;
   for (int64_t o = 0; o < a.B; o += NT) {
     if (a.B > NT) {
-      mine = o + tid < a.B ? tiles_of(a.Hkv, request(a, o + tid)) : 0;
+      mine = o + tid < a.B ? places_of(a.Hkv, request(a, o + tid)) : 0;
       int64_t s = mine;
       for (int d = 1; d < 64; d *= 2) {
         const int64_t y = __shfl_up(s, d);
@@ -308,10 +313,9 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
     if (base > at) break;
   }
   __syncthreads();
-  const int64_t count = end - at;
   if (tid == 0) {
     const int64_t b = found[0];
-    cursor = Cursor{at, end, b, found[1], request(a, b)};
+    cursors[0] = Cursor{at, b, found[1], request(a, b)};
   }
   __syncthreads();
 
@@ -327,7 +331,10 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   const uint32_t tile_at = __builtin_amdgcn_readfirstlane(
       uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)tile)));
   // ---- the fetching side: S - 1 tiles ahead, over the ends of items
-  int f_t = 0, f_t1 = 0, f_seg = 0, f_len = 0, f_keys = 0, f_batch = 0;
+  int f_t = 0, f_t1 = 0, f_len = 0, f_keys = 0, f_batch = 0, f_tiles = S;
+  int prepared = 0, f_seg = 0;  // shares prepared, the next one to fetch
+  int turn = 0;                 // which cursor holds
+  bool more = true;
   const char *f_head = nullptr, *f_node = nullptr;
   const int32_t* f_table = nullptr;
   const char* const zero = reinterpret_cast<const char*>(&zero_piece);
@@ -341,74 +348,100 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   constexpr bool SAME = NT / CPR % 16 == 0;
   const int lane_row = lane / CPR;
   // The rows of a wavefront's load lie in one page, so its page ids are UNITS a
-  // tile. A register holds those of BATCH tiles, one a lane; the next BATCH are
-  // on their way to LDS meanwhile (they have landed by then: BATCH >= S).
+  // tile. A register holds those of BATCH tiles, one a lane; the next BATCH (box
+  // 0) and the first of the next share (box 1) are on their way to LDS meanwhile.
   const bool one_page = (WROWS >> page_shift) <= 1;
   constexpr int BATCH = 64 / UNITS;
-  static_assert(BATCH >= S && UNITS <= 64, "a batch of page ids lands in time");
+  static_assert(BATCH >= S && UNITS <= 64, "a batch of page ids lands before its use");
   int32_t ids = 0;
-  const uint32_t id_at = uniform(
-      int(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)&id_box[wv][0])));
+  const uint32_t id_at = uniform(int(reinterpret_cast<uintptr_t>(
+      (__attribute__((address_space(3))) char*)&id_box[wv][0][0])));
   // this lane's page id in the batch of tiles from t on (the prefix's last at most)
-  auto id_place = [&](int t) {
+  auto id_place = [&](const int32_t* table, int t, int len) {
     const int key = (t + lane / UNITS) * KT + lane % UNITS * (NT / CPR) + wv * WROWS;
-    return f_table + ((key < f_len ? key : f_len - 1) >> page_shift);
+    return table + ((key < len ? key : len - 1) >> page_shift);
+  };
+  auto take_ids = [&](int box) {
+    ids = id_box[wv][box][lane];
+    asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(ids) : : "memory");
   };
 
-  auto next_segment = [&]() {
+  // Finds the next share of this worker, with its first page ids on their way.
+  auto prepare = [&]() {
     const Args s = seldom();
-    meet();  // the cursor is written
+    const Cursor& cursor = cursors[turn];
     int64_t at = uniform(cursor.at), b = uniform(cursor.b), b_first = uniform(cursor.b_first);
-    const int64_t end = uniform(cursor.end);
     Req rq{uniform(cursor.rq.first), uniform(cursor.rq.n), uniform(cursor.rq.len),
            uniform(cursor.rq.tiles), uniform(cursor.rq.row_tiles)};
-    while (at >= b_first + tiles_of(s->Hkv, rq)) {
-      b_first += tiles_of(s->Hkv, rq);
-      rq = uniform_request(s, ++b);
-    }
-    const int64_t into = at - b_first;
-    const int item = int(into / rq.tiles);  // (key head, row tile)
     Seg sg;
-    sg.t0 = int(into - int64_t(item) * rq.tiles);
-    sg.t1 = int(rq.tiles - sg.t0 < end - at ? rq.tiles : sg.t0 + (end - at));
-    sg.start = at - sg.t0;
+    do {
+      if (at >= end) {
+        more = false;
+        return;
+      }
+      while (at >= b_first + places_of(s->Hkv, rq)) {
+        b_first += places_of(s->Hkv, rq);
+        rq = uniform_request(s, ++b);
+      }
+      const int64_t into = at - b_first;
+      const int size = rq.tiles + kItemPlaces;
+      const int item = int(into / size);  // (key head, row tile)
+      const int p0 = int(into - int64_t(item) * size);
+      const int p1 = int(size - p0 < end - at ? size : p0 + (end - at));
+      sg.start = at - p0;
+      sg.t0 = min(p0, rq.tiles);
+      sg.t1 = min(p1, rq.tiles);
+      sg.h = item / rq.row_tiles;
+      sg.rt = item - sg.h * rq.row_tiles;
+      at += p1 - p0;
+    } while (sg.t0 == sg.t1);
     sg.first = rq.first;
     sg.n = rq.n;
     sg.len = rq.len;
-    sg.h = item / rq.row_tiles;
-    sg.rt = item - sg.h * rq.row_tiles;
     sg.tiles = rq.tiles;
-    at += sg.t1 - sg.t0;
-    meet();  // everyone has read the cursor
+    sg.head = int64_t(s->k_cache + sg.h * s->c_h);
+    sg.node = int64_t(s->k_tree + rq.first * s->n_t + sg.h * s->n_h);
+    const int32_t* table = s->table + b * s->table_stride;
+    sg.table = int64_t(table);
+    if (one_page && rq.len > 0) load_lds4(id_place(table, sg.t0, rq.len), id_at + 256);
+    turn ^= 1;
     if (tid == 0) {
-      segs[f_seg % S] = sg;
-      cursor = Cursor{at, end, b, b_first, rq};
+      segs[prepared % (S + 2)] = sg;
+      cursors[turn] = Cursor{at, b, b_first, rq};
     }
-    ++f_seg;
-    f_t = sg.t0;
-    f_t1 = sg.t1;
-    f_len = rq.len;
-    f_keys = rq.len + rq.n;
-    f_head = s->k_cache + sg.h * s->c_h;
-    f_node = s->k_tree + rq.first * s->n_t + sg.h * s->n_h;
-    f_table = s->table + b * s->table_stride;
-    f_batch = f_t;
-    if (one_page && f_len > 0) {
-      ids = *id_place(f_t);
-      if (f_t + BATCH < f_t1) load_lds4(id_place(f_t + BATCH), id_at);
-    }
+    ++prepared;
   };
-  // Starts the next tile's keys and values on their way into a stage.
+  // Starts the next tile's keys and values on their way into a stage; false when
+  // the share is at its end.
   auto fetch_next = [&](int to_stage) {
-    if (f_t == f_t1) next_segment();
+    const bool fresh = f_t == f_t1;
+    if (fresh) {
+      if (!more) return false;
+      const Seg& sg = segs[f_seg % (S + 2)];
+      ++f_seg;
+      f_t = uniform(sg.t0);
+      f_t1 = uniform(sg.t1);
+      f_len = uniform(sg.len);
+      f_keys = f_len + uniform(sg.n);
+      f_head = reinterpret_cast<const char*>(uniform(sg.head));
+      f_node = reinterpret_cast<const char*>(uniform(sg.node));
+      f_table = reinterpret_cast<const int32_t*>(uniform(sg.table));
+      f_batch = f_t;
+      if (one_page && f_len > 0) {
+        // its ids are older than the tiles of the share before but the first
+        if (f_tiles < S) asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+        take_ids(1);
+        if (f_t + BATCH < f_t1) load_lds4(id_place(f_table, f_t + BATCH, f_len), id_at);
+      }
+      f_tiles = f_t1 - f_t;
+    }
     const int t = f_t++;
     const uint32_t stage = tile_at + uint32_t(to_stage) * STAGE + wv * 1024;
     if (t - f_batch == BATCH) {
       f_batch = t;
       if (one_page && f_len > 0) {
-        ids = id_box[wv][lane];
-        asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(ids) : : "memory");
-        if (t + BATCH < f_t1) load_lds4(id_place(t + BATCH), id_at);
+        take_ids(0);
+        if (t + BATCH < f_t1) load_lds4(id_place(f_table, t + BATCH, f_len), id_at);
       }
     }
     const int id0 = (t - f_batch) * UNITS;
@@ -464,6 +497,8 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
         load_lds16(some ? vp : zero, stage + u * NT * 16 + KT * DP * 2);
       }
     }
+    if (fresh) prepare();
+    return true;
   };
 
   // ---- the computing side
@@ -472,29 +507,73 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   int hq = 0, node = 0, wild = 0;
   bool row_ok = false, wave_ok = false;
   uint64_t see0 = 0, see1 = 0;
-  typename E::vec qf[DP / 16];
+  u32x4 qf[DP / 16];
   f32x16 acc[ND];
   float m = -INFINITY, l = 0.0f;
 
+  // The rows of share `which`: this lane's part of them to registers, and its mask.
+  uint64_t next_see0 = 0, next_see1 = 0;
+  auto load_rows = [&](int which) {
+    const Args s = seldom();
+    const Seg& sg = segs[which % (S + 2)];
+    const int n = uniform(sg.n), h = uniform(sg.h), row0 = uniform(sg.rt) * M + rw * 32;
+    if (row0 >= n * s->G) return;
+    const int r = row0 + col < n * s->G ? row0 + col : 0;
+    const int node = r / s->G;
+    const int64_t i = uniform(sg.first) + node;
+    const char* qp = s->q + i * s->q_t + (h * s->G + r - node * s->G) * s->q_h;
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k) {
+      const int d = 16 * k + 8 * half;
+      u32x4 x = {0, 0, 0, 0};
+      if (d < s->D) x = *reinterpret_cast<const u32x4*>(qp + d * 2);
+      qf[k] = x;
+    }
+    if (s->anc) {
+      const uint64_t* words = s->anc + i * s->words;
+      next_see0 = words[0];
+      next_see1 = s->words > 1 ? words[1] : 0;
+    } else {
+      next_see0 = node >= 63 ? ~uint64_t(0) : (uint64_t(2) << node) - 1;
+      next_see1 = node < 64 ? 0 : node >= 127 ? ~uint64_t(0) : (uint64_t(2) << (node - 64)) - 1;
+    }
+  };
+
+  // They are asked for when a share ends, and here before its results are
+  // written: where the loop over tiles began with them on their way, the
+  // compiler would wait for every load in it.
+  auto rows_here = [&]() {
+#pragma unroll
+    for (int k = 0; k < DP / 16; ++k) asm volatile("" : "+v"(qf[k]));
+    asm volatile("" : "+v"(next_see0), "+v"(next_see1));
+  };
+
+  prepare();
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+  meet();
+  if (more) load_rows(0);
+  rows_here();
+  int fetched = 0, done = 0;
 #pragma unroll 1
-  for (int i = 0; i < S - 1; ++i)
-    if (i < count) fetch_next(i);
+  for (int i = 0; i < S - 1; ++i) {
+    if (fetch_next(i)) ++fetched;
+    meet();
+  }
   int st_now = 0, st_next = S - 1;  // stages of this tile and of the one to fetch
-  for (int64_t left = count; left > 0; --left) {
+  for (; done < fetched; ++done) {
     // this tile is here; everyone is done with the one before, whose stage is next
-    if (S >= 4 && left > 2) wait_and_meet<2 * LOADS>();
-    else if (S >= 3 && left > 1) wait_and_meet<LOADS>();
+    if (S >= 4 && fetched - done > 2) wait_and_meet<2 * LOADS>();
+    else if (S >= 3 && fetched - done > 1) wait_and_meet<LOADS>();
     else wait_and_meet<0>();
 
     if (t == t1) {
       const Args s = seldom();
-      const Seg& sg = segs[seg % S];
+      const Seg& sg = segs[seg % (S + 2)];
       t = uniform(sg.t0);
       t1 = uniform(sg.t1);
       len = uniform(sg.len);
       n = uniform(sg.n);
       const int h = uniform(sg.h), rt = uniform(sg.rt);
-      const int64_t first = uniform(sg.first);
       keys = len + n;
       ++seg;
       const int r = rt * M + rw * 32 + col;
@@ -502,37 +581,17 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
       node = row_ok ? r / s->G : 0;
       hq = h * s->G + (row_ok ? r - node * s->G : 0);
       wave_ok = rt * M + rw * 32 < n * s->G;
-      see0 = see1 = 0;
-      if (wave_ok) {
-        const char* qp = s->q + (first + node) * s->q_t + hq * s->q_h;
-#pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-          const int d = 16 * k + 8 * half;
-          u32x4 x = {0, 0, 0, 0};
-          if (d < s->D) x = *reinterpret_cast<const u32x4*>(qp + d * 2);
-          qf[k] = __builtin_bit_cast(typename E::vec, x);
-        }
-        if (s->anc) {
-          const uint64_t* words = s->anc + (first + node) * s->words;
-          see0 = words[0];
-          if (s->words > 1) see1 = words[1];
-        } else {
-          see0 = node >= 63 ? ~uint64_t(0) : (uint64_t(2) << node) - 1;
-          see1 = node < 64 ? 0 : node >= 127 ? ~uint64_t(0) : (uint64_t(2) << (node - 64)) - 1;
-        }
-        // bits behind the tree are none of its nodes
-        see0 &= n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1;
-        see1 &= n >= 128 ? ~uint64_t(0) : n <= 64 ? 0 : (uint64_t(1) << (n - 64)) - 1;
-      }
+      // bits behind the tree are none of its nodes
+      see0 = next_see0 & (n >= 64 ? ~uint64_t(0) : (uint64_t(1) << n) - 1);
+      see1 = next_see1 &
+             (n >= 128 ? ~uint64_t(0) : n <= 64 ? 0 : (uint64_t(1) << (n - 64)) - 1);
 #pragma unroll
       for (int i = 0; i < ND; ++i) acc[i] = f32x16{0};
       m = -INFINITY;
       l = 0.0f;
       wild = 0;
-      // the rows have to come before further tiles queue in front of them
-      asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
     }
-    if (left > S - 1) fetch_next(st_next);
+    if (fetch_next(st_next)) ++fetched;
     char* const tv = tile + st_now * STAGE + KT * DP * 2;
     const uint32_t stage = tile_at + uint32_t(st_now) * STAGE;
     // Nodes' values that are infinite or NaN would reach the rows that do not
@@ -578,7 +637,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
                 ((stage + k_off) ^ ((k8 + i) * 32)) + nb * 32 * (DP * 2));
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int i = 0; i < STEP; ++i) s[nb] = E::mfma(kf[i], qf[k8 + i], s[nb]);
+          for (int i = 0; i < STEP; ++i) s[nb] = E::mfma(kf[i], __builtin_bit_cast(typename E::vec, qf[k8 + i]), s[nb]);
         }
       }
       // V^T of a half block of keys: columns d of this lane, keys in the order
@@ -650,8 +709,9 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
     }
     ++t;
     if (t == t1) {
+      if (fetched - done > 1) load_rows(seg);
       const Args s = seldom();
-      const Seg& sg = segs[(seg - 1) % S];
+      const Seg& sg = segs[(seg - 1) % (S + 2)];
       const int t0 = uniform(sg.t0), h = uniform(sg.h);
       const int64_t first = uniform(sg.first);
       const bool whole = t0 == 0 && t1 == uniform(sg.tiles);
@@ -736,6 +796,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
         }
       }
 
+      rows_here();
       if (kw == 0 && row_ok) {
         if (whole) {
           const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
