@@ -9,12 +9,11 @@ waits for the GPU, and all of them can be captured into a graph.
 from __future__ import annotations
 
 import ctypes
-from contextlib import nullcontext
 from dataclasses import dataclass
 
 import torch
 
-from . import (SV_BF16, SV_ERR_ROW, SV_ERR_TOKEN, SV_F32, SpecVerifyError, _check, _need, _ptr,
+from . import (SV_BF16, SV_ERR_ROW, SV_ERR_TOKEN, SV_F32, SpecVerifyError, _check,  # noqa: F401
                load_library)
 
 SV_F16 = 2
@@ -62,29 +61,51 @@ def _lib() -> ctypes.CDLL:
     return lib
 
 
-def _on(device: torch.device):
-    """The device of the tensors as the current one, as the C entry points ask."""
-    return nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+_current_device = torch._C._cuda_getDevice            # torch.cuda.current_device and
+_raw_stream = torch._C._cuda_getCurrentRawStream       # current_stream without their wrappers
 
 
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _call(name: str, device: torch.device, *args) -> None:
+    """Enqueues on the tensors' device's current stream, with that device current as the C entry
+    points ask."""
+    index = device.index
+    fn = getattr(_bound, name)
+    if _current_device() == index:
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _raw_stream(index))
+    if st:
+        _check(st, name)
 
 
-def _same_device(device: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise SpecVerifyError(f"{name} is on {t.device}, the others on {device}")
+def _want(t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: torch.device, name: str) -> None:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != dev:
+        raise SpecVerifyError(f"{name}: want contiguous {dtype} {tuple(shape)} on {dev}, got "
+                              f"{t.dtype} {tuple(t.shape)} contiguous={t.is_contiguous()} on "
+                              f"{t.device}")
 
 
-def _strided(t: torch.Tensor, ndim: int, name: str) -> None:
-    if not t.is_cuda or t.dim() != ndim or (t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise SpecVerifyError(f"{name}: want a {ndim}-d device tensor with a contiguous last axis")
+def _strided(t: torch.Tensor, dev: torch.device, ndim: int, name: str) -> tuple:
+    """The strides of a tensor whose last axis is contiguous."""
+    strides = t.stride()
+    if len(strides) != ndim or (strides[-1] != 1 and t.shape[-1] > 1 and t.numel()) or t.device != dev:
+        raise SpecVerifyError(f"{name}: want a {ndim}-d tensor on {dev} with a contiguous last axis")
+    return strides
 
 
-def _same_layout(a: torch.Tensor, b: torch.Tensor, names: str) -> None:
-    if a.shape != b.shape or a.stride() != b.stride() or a.dtype != b.dtype:
-        raise SpecVerifyError(f"{names} differ in shape, strides or type")
+def _device(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise SpecVerifyError(f"{name} must be a device tensor")
+    return t.device
+
+
+def _pair(a: torch.Tensor, b: torch.Tensor, dev: torch.device, ndim: int, names: str) -> tuple:
+    """The strides that two tensors of one shape and type share."""
+    strides = _strided(a, dev, ndim, names)
+    if a.shape != b.shape or strides != b.stride() or a.dtype is not b.dtype or b.device != dev:
+        raise SpecVerifyError(f"{names} differ in shape, strides, type or device")
+    return strides
 
 
 def _dtype(t: torch.Tensor, allowed: tuple, name: str) -> int:
@@ -93,9 +114,31 @@ def _dtype(t: torch.Tensor, allowed: tuple, name: str) -> int:
     return _DTYPES[t.dtype]
 
 
-def _error_word(t: torch.Tensor | None) -> None:
-    if t is not None:
-        _need(t, torch.int32, (1,), "device_error")
+def _table(t: torch.Tensor, B: int, dev: torch.device) -> tuple:
+    """(max_pages, row stride) of a block table."""
+    stride = _strided(t, dev, 2, "block_table")[0]
+    rows, width = t.shape
+    if t.dtype is not torch.int32 or rows != B:
+        raise SpecVerifyError(f"block_table: want int32 [{B}, max_pages]")
+    return width, max(width, stride)
+
+
+def _optional(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, dev: torch.device,
+              name: str) -> int | None:
+    if t is None:
+        return None
+    _want(t, dtype, shape, dev, name)
+    return t.data_ptr()
+
+
+def _scratch(ws: torch.Tensor | None, nbytes: int, dev: torch.device, name: str) -> torch.Tensor:
+    if nbytes == 0:
+        raise SpecVerifyError(f"sizes rejected by {name}")
+    if ws is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)  # any contents will do
+    if ws.device != dev:
+        raise SpecVerifyError(f"ws is on {ws.device}, the tensors on {dev}")
+    return ws
 
 
 @dataclass
@@ -115,49 +158,37 @@ def specverify_tree_plan(parents: torch.Tensor, node_start: torch.Tensor, prefix
                          device_error: torch.Tensor | None = None) -> TreePlanOutputs:
     """Ancestor masks, depths, positions, and room in the cache: block_table [B, max_pages] int32
     is filled in place with pages from free_pages[free_head:], the rest comes back new."""
-    lib = _lib()
-    dev = parents.device
-    T, B = parents.numel(), prefix_len.numel()
-    _need(parents, torch.int32, (T,), "parents")
-    _need(node_start, torch.int32, (B + 1,), "node_start")
-    _need(prefix_len, torch.int32, (B,), "prefix_len")
-    _need(pages, torch.int32, (B,), "pages")
-    _need(free_pages, torch.int32, (free_pages.numel(),), "free_pages")
-    _need(free_head, torch.int32, (1,), "free_head")
-    _strided(block_table, 2, "block_table")
-    if block_table.dtype != torch.int32 or block_table.shape[0] != B:
-        raise SpecVerifyError(f"block_table: want int32 [{B}, max_pages]")
-    _error_word(device_error)
-    _same_device(dev, node_start=node_start, prefix_len=prefix_len, pages=pages,
-                 block_table=block_table, free_pages=free_pages, free_head=free_head,
-                 device_error=device_error)
-    words = (max_nodes + 63) // 64
-    out = TreePlanOutputs(
-        ancestors=torch.empty((T, words), dtype=torch.int64, device=dev),
-        depth=torch.empty(T, dtype=torch.int32, device=dev),
-        position=torch.empty(T, dtype=torch.int32, device=dev),
-        slots=torch.empty((B, max(max_path, 0)), dtype=torch.int64, device=dev),
-        pages=torch.empty(B, dtype=torch.int32, device=dev),
-        free_head=torch.empty(1, dtype=torch.int32, device=dev))
-    width = block_table.shape[1]
-    with _on(dev):
-        st = lib.specverify_tree_plan(
-            parents.data_ptr(), node_start.data_ptr(), prefix_len.data_ptr(), pages.data_ptr(),
-            block_table.data_ptr(), free_pages.data_ptr(), free_head.data_ptr(), B, T, max_nodes,
-            max_path, page_size, width, max(width, block_table.stride(0)), num_pages,
-            free_pages.numel(), out.ancestors.data_ptr(), out.depth.data_ptr(),
-            out.position.data_ptr(), out.slots.data_ptr(), out.pages.data_ptr(),
-            out.free_head.data_ptr(), _ptr(device_error), _stream(dev))
-    _check(st, "specverify_tree_plan")
-    return out
+    _lib()
+    dev = _device(parents, "parents")
+    T, B, free = parents.numel(), prefix_len.numel(), free_pages.numel()
+    i32 = torch.int32
+    _want(parents, i32, (T,), dev, "parents")
+    _want(node_start, i32, (B + 1,), dev, "node_start")
+    _want(prefix_len, i32, (B,), dev, "prefix_len")
+    _want(pages, i32, (B,), dev, "pages")
+    _want(free_pages, i32, (free,), dev, "free_pages")
+    _want(free_head, i32, (1,), dev, "free_head")
+    width, stride = _table(block_table, B, dev)
+    err = _optional(device_error, i32, (1,), dev, "device_error")
+    empty = torch.empty
+    ancestors = empty((T, (max_nodes + 63) // 64), dtype=torch.int64, device=dev)
+    depth = empty(T, dtype=i32, device=dev)
+    position = empty(T, dtype=i32, device=dev)
+    slots = empty((B, max(max_path, 0)), dtype=torch.int64, device=dev)
+    now = empty(B, dtype=i32, device=dev)
+    head = empty(1, dtype=i32, device=dev)
+    _call("specverify_tree_plan", dev, parents.data_ptr(), node_start.data_ptr(),
+          prefix_len.data_ptr(), pages.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
+          free_head.data_ptr(), B, T, max_nodes, max_path, page_size, width, stride, num_pages,
+          free, ancestors.data_ptr(), depth.data_ptr(), position.data_ptr(), slots.data_ptr(),
+          now.data_ptr(), head.data_ptr(), err)
+    return TreePlanOutputs(ancestors, depth, position, slots, now, head)
 
 
 def tree_attention_workspace(B: int, T: int, Hq: int, Hkv: int, D: int, max_nodes: int,
                              device) -> torch.Tensor:
     n = int(_lib().specverify_tree_attention_workspace_size(B, T, Hq, Hkv, D, max_nodes))
-    if n == 0:
-        raise SpecVerifyError("sizes rejected by specverify_tree_attention_workspace_size")
-    return torch.empty(n, dtype=torch.uint8, device=device)  # any contents will do
+    return _scratch(None, n, device, "specverify_tree_attention_workspace_size")
 
 
 def specverify_tree_attention(q: torch.Tensor, k_tree: torch.Tensor, v_tree: torch.Tensor,
@@ -175,51 +206,38 @@ def specverify_tree_attention(q: torch.Tensor, k_tree: torch.Tensor, v_tree: tor
     and values' strides agree), ancestors [T, ceil(max_nodes / 64)] int64 or None for chains,
     scale 1 / sqrt(D) if not given."""
     lib = _lib()
-    for t, ndim, name in ((q, 3, "q"), (k_tree, 3, "k_tree"), (v_tree, 3, "v_tree"),
-                          (k_cache, 4, "k_cache"), (v_cache, 4, "v_cache")):
-        _strided(t, ndim, name)
-    _same_layout(k_tree, v_tree, "k_tree and v_tree")
-    _same_layout(k_cache, v_cache, "k_cache and v_cache")
-    dev = q.device
+    dev = _device(q, "q")
+    qs = _strided(q, dev, 3, "q")
+    ns = _pair(k_tree, v_tree, dev, 3, "k_tree and v_tree")
+    cs = _pair(k_cache, v_cache, dev, 4, "k_cache and v_cache")
     T, Hq, D = q.shape
-    num_pages, page_size, Hkv = k_cache.shape[:3]
+    num_pages, page_size, Hkv, width = k_cache.shape
     B = prefix_len.numel()
-    if k_tree.shape != (T, Hkv, D) or k_cache.shape[3] != D:
-        raise SpecVerifyError("q [T, Hq, D], k_tree [T, Hkv, D] and k_cache [.., .., Hkv, D] disagree")
+    if k_tree.shape != (T, Hkv, D) or width != D:
+        raise SpecVerifyError("q [T, Hq, D], k_tree [T, Hkv, D] and k_cache [pages, page_size, Hkv, "
+                              "D] disagree")
     dt = _dtype(q, (torch.bfloat16, torch.float16), "q")
-    if k_tree.dtype != q.dtype or k_cache.dtype != q.dtype:
+    if k_tree.dtype is not q.dtype or k_cache.dtype is not q.dtype:
         raise SpecVerifyError("q, the nodes' and the cache's types differ")
-    _need(prefix_len, torch.int32, (B,), "prefix_len")
-    _need(node_start, torch.int32, (B + 1,), "node_start")
-    _strided(block_table, 2, "block_table")
-    if block_table.dtype != torch.int32 or block_table.shape[0] != B:
-        raise SpecVerifyError(f"block_table: want int32 [{B}, max_pages]")
-    if ancestors is not None:
-        _need(ancestors, torch.int64, (T, (max_nodes + 63) // 64), "ancestors")
+    _want(prefix_len, torch.int32, (B,), dev, "prefix_len")
+    _want(node_start, torch.int32, (B + 1,), dev, "node_start")
+    max_pages, table_stride = _table(block_table, B, dev)
+    anc = _optional(ancestors, torch.int64, (T, (max_nodes + 63) // 64), dev, "ancestors")
     if out is None:
         out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
-    else:
-        _strided(out, 3, "out")
-        if out.shape != (T, Hq, D) or out.dtype != q.dtype:
-            raise SpecVerifyError(f"out: want {q.dtype} [{T}, {Hq}, {D}]")
-    _error_word(device_error)
-    _same_device(dev, k_tree=k_tree, v_tree=v_tree, k_cache=k_cache, v_cache=v_cache,
-                 block_table=block_table, prefix_len=prefix_len, node_start=node_start,
-                 ancestors=ancestors, out=out, device_error=device_error, ws=ws)
+    elif out.shape != (T, Hq, D) or out.dtype is not q.dtype:
+        raise SpecVerifyError(f"out: want {q.dtype} [{T}, {Hq}, {D}]")
+    os_ = _strided(out, dev, 3, "out")
+    err = _optional(device_error, torch.int32, (1,), dev, "device_error")
     lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if want_lse else None
-    if ws is None:
-        ws = tree_attention_workspace(B, T, Hq, Hkv, D, max_nodes, dev)
-    width = block_table.shape[1]
-    qs, ns, cs, os_ = q.stride(), k_tree.stride(), k_cache.stride(), out.stride()
-    with _on(dev):
-        st = lib.specverify_tree_attention(
-            q.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), dt, B, T, Hq, Hkv, D, max_nodes, qs[0], qs[1], ns[0], ns[1], cs[0],
-            cs[1], cs[2], num_pages, page_size, block_table.data_ptr(), width,
-            max(width, block_table.stride(0)), prefix_len.data_ptr(), node_start.data_ptr(),
-            _ptr(ancestors), D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1],
-            _ptr(lse), _ptr(device_error), ws.data_ptr(), ws.numel(), _stream(dev))
-    _check(st, "specverify_tree_attention")
+    ws = _scratch(ws, lib.specverify_tree_attention_workspace_size(B, T, Hq, Hkv, D, max_nodes),
+                  dev, "specverify_tree_attention_workspace_size")
+    _call("specverify_tree_attention", dev, q.data_ptr(), k_tree.data_ptr(), v_tree.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr(), dt, B, T, Hq, Hkv, D, max_nodes, qs[0], qs[1],
+          ns[0], ns[1], cs[0], cs[1], cs[2], num_pages, page_size, block_table.data_ptr(),
+          max_pages, table_stride, prefix_len.data_ptr(), node_start.data_ptr(), anc,
+          D ** -0.5 if scale is None else scale, out.data_ptr(), os_[0], os_[1],
+          lse.data_ptr() if want_lse else None, err, ws.data_ptr(), ws.numel())
     return out, lse
 
 
@@ -233,9 +251,7 @@ class TreeVerifyOutputs:
 
 def tree_verify_workspace(B: int, V: int, max_nodes: int, device) -> torch.Tensor:
     n = int(_lib().specverify_tree_verify_workspace_size(B, V, max_nodes))
-    if n == 0:
-        raise SpecVerifyError("sizes rejected by specverify_tree_verify_workspace_size")
-    return torch.empty(n, dtype=torch.uint8, device=device)  # any contents will do
+    return _scratch(None, n, device, "specverify_tree_verify_workspace_size")
 
 
 def specverify_tree_verify(target_probs: torch.Tensor, draft_probs: torch.Tensor | None,
@@ -248,40 +264,36 @@ def specverify_tree_verify(target_probs: torch.Tensor, draft_probs: torch.Tensor
     target_probs and draft_probs [T, V] (float32 or bfloat16, last axis contiguous; draft_probs
     None for DRAFT_FIXED), tokens and parents [T] int32, u [T] and r [B] float64 in [0, 1)."""
     lib = _lib()
-    _strided(target_probs, 2, "target_probs")
+    dev = _device(target_probs, "target_probs")
+    t_stride = _strided(target_probs, dev, 2, "target_probs")[0]
     T, V = target_probs.shape
     B = r.numel()
-    dev = target_probs.device
     dt = _dtype(target_probs, (torch.float32, torch.bfloat16), "target_probs")
+    q, d_stride = None, 0
     if draft_probs is not None:
-        _strided(draft_probs, 2, "draft_probs")
-        if draft_probs.shape != (T, V) or draft_probs.dtype != target_probs.dtype:
+        d_stride = _strided(draft_probs, dev, 2, "draft_probs")[0]
+        if draft_probs.shape != (T, V) or draft_probs.dtype is not target_probs.dtype:
             raise SpecVerifyError(f"draft_probs: want {target_probs.dtype} [{T}, {V}]")
-    _need(tokens, torch.int32, (T,), "tokens")
-    _need(parents, torch.int32, (T,), "parents")
-    _need(node_start, torch.int32, (B + 1,), "node_start")
-    _need(u, torch.float64, (T,), "u")
-    _need(r, torch.float64, (B,), "r")
-    _error_word(device_error)
-    _same_device(dev, draft_probs=draft_probs, tokens=tokens, parents=parents,
-                 node_start=node_start, u=u, r=r, device_error=device_error, ws=ws)
+        q = draft_probs.data_ptr()
+    i32 = torch.int32
+    _want(tokens, i32, (T,), dev, "tokens")
+    _want(parents, i32, (T,), dev, "parents")
+    _want(node_start, i32, (B + 1,), dev, "node_start")
+    _want(u, torch.float64, (T,), dev, "u")
+    _want(r, torch.float64, (B,), dev, "r")
+    err = _optional(device_error, i32, (1,), dev, "device_error")
     width = max(max_path, 0)
-    out = TreeVerifyOutputs(accept_len=torch.empty(B, dtype=torch.int32, device=dev),
-                            path=torch.empty((B, width), dtype=torch.int32, device=dev),
-                            emitted=torch.empty((B, width), dtype=torch.int32, device=dev),
-                            out_token=torch.empty(B, dtype=torch.int32, device=dev))
-    if ws is None:
-        ws = tree_verify_workspace(B, V, max_nodes, dev)
-    with _on(dev):
-        st = lib.specverify_tree_verify(
-            target_probs.data_ptr(), _ptr(draft_probs), dt, mode, tokens.data_ptr(),
-            parents.data_ptr(), node_start.data_ptr(), B, T, V, max_nodes, max_path,
-            target_probs.stride(0), 0 if draft_probs is None else draft_probs.stride(0),
-            u.data_ptr(), r.data_ptr(), out.accept_len.data_ptr(), out.path.data_ptr(),
-            out.emitted.data_ptr(), out.out_token.data_ptr(), _ptr(device_error), ws.data_ptr(),
-            ws.numel(), _stream(dev))
-    _check(st, "specverify_tree_verify")
-    return out
+    accept_len = torch.empty(B, dtype=i32, device=dev)
+    path = torch.empty((B, width), dtype=i32, device=dev)
+    emitted = torch.empty((B, width), dtype=i32, device=dev)
+    out_token = torch.empty(B, dtype=i32, device=dev)
+    ws = _scratch(ws, lib.specverify_tree_verify_workspace_size(B, V, max_nodes), dev,
+                  "specverify_tree_verify_workspace_size")
+    _call("specverify_tree_verify", dev, target_probs.data_ptr(), q, dt, mode, tokens.data_ptr(),
+          parents.data_ptr(), node_start.data_ptr(), B, T, V, max_nodes, max_path, t_stride,
+          d_stride, u.data_ptr(), r.data_ptr(), accept_len.data_ptr(), path.data_ptr(),
+          emitted.data_ptr(), out_token.data_ptr(), err, ws.data_ptr(), ws.numel())
+    return TreeVerifyOutputs(accept_len, path, emitted, out_token)
 
 
 def specverify_tree_commit(k_tree: torch.Tensor, v_tree: torch.Tensor, k_cache: torch.Tensor,
@@ -294,41 +306,31 @@ def specverify_tree_commit(k_tree: torch.Tensor, v_tree: torch.Tensor, k_cache: 
 
     k_tree and v_tree [layers, T, H, D], k_cache and v_cache [layers, num_pages, page_size, H, D]
     (float32, bfloat16 or float16, last axis contiguous, other strides multiples of 16 bytes)."""
-    lib = _lib()
-    for t, ndim, name in ((k_tree, 4, "k_tree"), (v_tree, 4, "v_tree"), (k_cache, 5, "k_cache"),
-                          (v_cache, 5, "v_cache")):
-        _strided(t, ndim, name)
-    _same_layout(k_tree, v_tree, "k_tree and v_tree")
-    _same_layout(k_cache, v_cache, "k_cache and v_cache")
+    _lib()
+    dev = _device(k_cache, "k_cache")
+    ns = _pair(k_tree, v_tree, dev, 4, "k_tree and v_tree")
+    cs = _pair(k_cache, v_cache, dev, 5, "k_cache and v_cache")
     L, T, H, D = k_tree.shape
-    num_pages, page_size = k_cache.shape[1:3]
-    if k_cache.shape[0] != L or k_cache.shape[3:] != (H, D) or k_cache.dtype != k_tree.dtype:
-        raise SpecVerifyError("k_tree [layers, T, H, D] and k_cache [layers, .., .., H, D] disagree")
+    layers, num_pages, page_size, heads, width = k_cache.shape
+    if layers != L or heads != H or width != D or k_cache.dtype is not k_tree.dtype:
+        raise SpecVerifyError("k_tree [layers, T, H, D] and k_cache [layers, pages, page_size, H, D] "
+                              "disagree")
     dt = _dtype(k_tree, tuple(_DTYPES), "k_tree")
-    B, dev = prefix_len.numel(), k_cache.device
-    if path.dim() != 2:
-        raise SpecVerifyError("path: want [B, max_path]")
-    max_path = path.shape[1]
-    _need(node_start, torch.int32, (B + 1,), "node_start")
-    _need(path, torch.int32, (B, max_path), "path")
-    _need(accept_len, torch.int32, (B,), "accept_len")
-    _need(slots, torch.int64, (B, max_path), "slots")
-    _need(prefix_len, torch.int32, (B,), "prefix_len")
+    B = prefix_len.numel()
+    max_path = path.shape[-1] if path.dim() else 0
+    i32 = torch.int32
+    _want(node_start, i32, (B + 1,), dev, "node_start")
+    _want(path, i32, (B, max_path), dev, "path")
+    _want(accept_len, i32, (B,), dev, "accept_len")
+    _want(slots, torch.int64, (B, max_path), dev, "slots")
+    _want(prefix_len, i32, (B,), dev, "prefix_len")
     if out is None:
-        out = torch.empty(B, dtype=torch.int32, device=dev)
+        out = torch.empty(B, dtype=i32, device=dev)
     else:
-        _need(out, torch.int32, (B,), "out")
-    _error_word(device_error)
-    _same_device(dev, k_tree=k_tree, v_tree=v_tree, v_cache=v_cache, node_start=node_start,
-                 path=path, accept_len=accept_len, slots=slots, prefix_len=prefix_len, out=out,
-                 device_error=device_error)
-    ns, cs = k_tree.stride(), k_cache.stride()
-    with _on(dev):
-        st = lib.specverify_tree_commit(
-            k_tree.data_ptr(), v_tree.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), dt, L, B,
-            T, H, D, max_nodes, max_path, ns[0], ns[1], ns[2], cs[0], cs[1], cs[2], cs[3],
-            num_pages, page_size, node_start.data_ptr(), path.data_ptr(), accept_len.data_ptr(),
-            slots.data_ptr(), prefix_len.data_ptr(), out.data_ptr(), _ptr(device_error),
-            _stream(dev))
-    _check(st, "specverify_tree_commit")
+        _want(out, i32, (B,), dev, "out")
+    err = _optional(device_error, i32, (1,), dev, "device_error")
+    _call("specverify_tree_commit", dev, k_tree.data_ptr(), v_tree.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), dt, L, B, T, H, D, max_nodes, max_path, ns[0], ns[1], ns[2], cs[0],
+          cs[1], cs[2], cs[3], num_pages, page_size, node_start.data_ptr(), path.data_ptr(),
+          accept_len.data_ptr(), slots.data_ptr(), prefix_len.data_ptr(), out.data_ptr(), err)
     return out
