@@ -18,11 +18,19 @@ namespace {
 
 using namespace svtree;
 
-constexpr int kBlock = 1024;
+constexpr int kBlock = 512;
 constexpr int kWaves = kBlock / kWave;
 constexpr int kVec = 8;                   // probabilities of a thread in a chunk
-constexpr int kChunk = kBlock * kVec;     // 8192
+constexpr int kChunk = kBlock * kVec;     // 4096
 constexpr int kMaxChunks = SV_MAX_TREE_VOCAB / kChunk;
+// Workgroups that a call is spread over at most: two to a CU, all resident when
+// the card is free.
+constexpr int kWorkers = 512;
+// What a workgroup waits for the others' sums, in ticks of the 100 MHz clock,
+// before it takes them itself.
+constexpr uint64_t kPatience = 2000;
+constexpr uint64_t kEmpty = ~uint64_t(0);           // a sum not yet there
+constexpr uint64_t kWrong = 0xFFF8000000000001ull;  // the chunk holds what is no probability
 
 struct VerifyArgs {
   const void* p;
@@ -35,6 +43,8 @@ struct VerifyArgs {
   const double* r;
   int64_t T, V;
   int max_nodes, max_path, mode;
+  int spread, chunks;  // workgroups of a request, chunks of a row
+  uint64_t* sums;      // [B][max_nodes + 1][chunks], kEmpty at the start (spread > 1)
   int32_t* accept_len;
   int32_t* path;
   int32_t* emitted;
@@ -55,30 +65,48 @@ __device__ __forceinline__ const void* row_at(const void* base, int64_t stride, 
   return static_cast<const char*>(base) + row * stride * (DT == SV_BF16 ? 2 : 4);
 }
 
-// 8 probabilities from v0 on as float32 (exact); 0 behind the row's end.
+// 8 probabilities from v0 on as float32 (exact); 0 behind the row's end. VEC: rows
+// begin at multiples of 16 bytes.
 template <int DT, bool VEC>
 __device__ __forceinline__ void load8(const void* row, int64_t v0, int64_t V, float (&x)[kVec]) {
-  if (VEC && v0 + kVec <= V) {
+  if (v0 + kVec <= V) {
     if constexpr (DT == SV_BF16) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(row) + v0);
+      const uint16_t* s = static_cast<const uint16_t*>(row) + v0;
+      u32x4 w;
+      if constexpr (VEC) {
+        w = *reinterpret_cast<const u32x4*>(s);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = uint32_t(s[2 * i]) | uint32_t(s[2 * i + 1]) << 16;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         x[2 * i] = __uint_as_float(w[i] << 16);
         x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
       }
     } else {
-      const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const float*>(row) + v0);
-      const u32x4 a = s[0], b = s[1];
+      const float* s = static_cast<const float*>(row) + v0;
+      if constexpr (VEC) {
+        const u32x4 a = reinterpret_cast<const u32x4*>(s)[0];
+        const u32x4 b = reinterpret_cast<const u32x4*>(s)[1];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = __uint_as_float(a[i]);
-        x[4 + i] = __uint_as_float(b[i]);
+        for (int i = 0; i < 4; ++i) {
+          x[i] = __uint_as_float(a[i]);
+          x[4 + i] = __uint_as_float(b[i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) x[i] = s[i];
       }
     }
   } else {
+#pragma unroll 1
+    for (int i = 0; i < kVec; ++i) {
+      const float y = v0 + i < V ? float(load_one<DT>(row, v0 + i)) : 0.0f;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
-      x[i] = v0 + i < V ? float(load_one<DT>(row, v0 + i)) : 0.0f;
+      for (int j = 0; j < kVec; ++j)
+        if (i == j) x[j] = y;
+    }
   }
 }
 
@@ -142,75 +170,137 @@ __device__ __forceinline__ double scan_wave(double x) {
 }
 
 struct Shared {
-  double chunk[kMaxChunks];   // mass of each chunk
-  double wave[2][kWaves];
+  double front[kMaxChunks];   // mass of the chunks up to and with each
+  double wave[4][kWaves];
   double px[SV_MAX_TREE_NODES], qx[SV_MAX_TREE_NODES], u[SV_MAX_TREE_NODES];
   int32_t tok[SV_MAX_TREE_NODES], up[SV_MAX_TREE_NODES];
-  double total;
-  int found;
+  int found, found_chunk;
 };
 
-// Mass of the weights: chunk sums to sm.chunk, their sum returned to every
-// thread. A thread adds its 8 ids in order, a wavefront and the workgroup scan
-// in a fixed order, chunks are added in order.
+// Masses of the chunks c .. c + kAtOnce - 1 below c1, as their bits or kWrong: of
+// chunk c + u to thread u. A thread adds its 8 ids in order, a wavefront and the
+// workgroup in a fixed order, so whichever workgroup takes a chunk gets the same
+// bits. Several at once, because one chunk's loads are not enough in flight.
+template <bool VEC>
+constexpr int kAtOnce = VEC ? 4 : 1;
 template <int DT, bool VEC>
-__device__ double mass_of(const Weights& w, int64_t V, Shared& sm, bool* ok) {
+__device__ __forceinline__ uint64_t chunk_masses(const Weights& w, int64_t V, Shared& sm, int c,
+                                                 int c1) {
   const int tid = int(threadIdx.x), lane = tid % kWave, wv = tid / kWave;
-  const int chunks = int((V + kChunk - 1) / kChunk);
-  bool good = true;
-  for (int c = 0; c < chunks; ++c) {
-    double x[kVec];
-    good = weigh<DT, VEC>(w, sm.tok, int64_t(c) * kChunk + tid * kVec, V, x) && good;
-    double s = 0.0;
+  double s[kAtOnce<VEC>];
+  bool good[kAtOnce<VEC>];
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) s += x[i];
-    s = scan_wave(s);
-    if (lane == kWave - 1) sm.wave[c & 1][wv] = s;
-    __syncthreads();
-    if (tid == 0) {
-      double t = 0.0;
-      for (int k = 0; k < kWaves; ++k) t += sm.wave[c & 1][k];
-      sm.chunk[c] = t;
+  for (int u = 0; u < kAtOnce<VEC>; ++u) {
+    double x[kVec];
+    // (behind the range: the row's last chunk again, not used)
+    const int64_t at = c + u < c1 ? c + u : c1 - 1;
+    good[u] = weigh<DT, VEC>(w, sm.tok, at * kChunk + tid * kVec, V, x);
+    s[u] = 0.0;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) s[u] += x[i];
+  }
+#pragma unroll
+  for (int u = 0; u < kAtOnce<VEC>; ++u) {
+    s[u] = scan_wave(s[u]);
+    if (__any(!good[u])) s[u] = __longlong_as_double((long long)kWrong);  // stays in every sum
+  }
+  __syncthreads();  // the sums before are read
+  if (lane == kWave - 1)
+#pragma unroll
+    for (int u = 0; u < kAtOnce<VEC>; ++u) sm.wave[u][wv] = s[u];
+  __syncthreads();
+  if (tid >= kAtOnce<VEC>) return kEmpty;
+  double t = 0.0;
+#pragma unroll
+  for (int k = 0; k < kWaves; ++k) t += sm.wave[tid][k];
+  return t != t ? kWrong : (uint64_t)__double_as_longlong(t);
+}
+
+// Mass of the weights: running sums of the chunks to sm.front, the whole
+// returned to every thread (NaN for a wrong row).
+//
+// The workgroups of a request run the same walk side by side; each takes its
+// share of a pass's chunks and publishes their sums, which are value and flag in
+// one 64-bit word. Nothing depends on all of them being resident at once: one
+// that has waited long enough takes what is missing itself (the same bits).
+template <int DT, bool VEC>
+__device__ __forceinline__ double mass_of(const VerifyArgs& a, const Weights& w, uint64_t* sums,
+                                          int share, Shared& sm) {
+  const int tid = int(threadIdx.x), lane = tid % kWave;
+  const int chunks = a.chunks;
+  int c0 = int(int64_t(chunks) * share / a.spread);
+  int c1 = int(int64_t(chunks) * (share + 1) / a.spread);
+  for (bool own = true;; own = false) {
+    for (int c = c0; c < c1; c += kAtOnce<VEC>) {
+      if (!own) {  // only where one is missing
+        bool there = true;
+        for (int u = c; u < c + kAtOnce<VEC> && u < c1; ++u)
+          there = there && (uint64_t)__double_as_longlong(sm.front[u]) != kEmpty;
+        if (there) continue;
+      }
+      const uint64_t s = chunk_masses<DT, VEC>(w, a.V, sm, c, c1);
+      if (tid < kAtOnce<VEC> && c + tid < c1) {
+        sm.front[c + tid] = __longlong_as_double((long long)s);
+        if (own && a.spread > 1)
+          __hip_atomic_store(sums + c + tid, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+    if (!own || a.spread == 1) break;
+    bool missing = false;
+    const uint64_t began = wall_clock64();
+    for (int c = tid; c < chunks; c += kBlock) {
+      if (c >= c0 && c < c1) continue;
+      uint64_t s = __hip_atomic_load(sums + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      while (s == kEmpty && wall_clock64() - began < kPatience) {
+        __builtin_amdgcn_s_sleep(1);
+        s = __hip_atomic_load(sums + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      missing = missing || s == kEmpty;
+      sm.front[c] = __longlong_as_double((long long)s);
+    }
+    if (!__syncthreads_or(missing)) break;
+    c0 = 0;
+    c1 = chunks;
+  }
+  __syncthreads();
+  if (tid < kWave) {
+    double before = 0.0;
+    for (int c = lane; c - lane < chunks; c += kWave) {
+      const double s = before + scan_wave(c < chunks ? sm.front[c] : 0.0);
+      if (c < chunks) sm.front[c] = s;
+      before = __shfl(s, kWave - 1);
     }
   }
-  *ok = !__syncthreads_or(!good);
-  if (tid == 0) {
-    double t = 0.0;
-    for (int c = 0; c < chunks; ++c) t += sm.chunk[c];
-    sm.total = t;
-  }
   __syncthreads();
-  const double t = sm.total;
-  __syncthreads();
-  return t;
+  return sm.front[chunks - 1];
 }
 
 // The least id whose running sum exceeds x, after mass_of of the same weights;
-// the last one with a weight when rounding leaves none.
+// the last one with a weight when rounding leaves none. -1 from a workgroup that
+// does not own the id's chunk.
 template <int DT, bool VEC>
-__device__ int32_t pick(const Weights& w, double x, int64_t V, Shared& sm) {
+__device__ int32_t pick(const VerifyArgs& a, const Weights& w, double x, int share, Shared& sm,
+                        bool* mine) {
   const int tid = int(threadIdx.x), lane = tid % kWave, wv = tid / kWave;
-  const int chunks = int((V + kChunk - 1) / kChunk);
-  // the chunk, and the mass in front of it (every thread for itself)
-  double front = 0.0, last_front = 0.0;
-  int c = 0, last = -1;
-  for (; c < chunks; ++c) {
-    const double s = sm.chunk[c];
-    if (front + s > x) break;
-    if (s > 0.0) {
-      last = c;
-      last_front = front;
+  const int chunks = a.chunks;
+  const double whole = sm.front[chunks - 1];
+  const bool over = !(x < whole);
+  if (tid == 0) sm.found_chunk = chunks - 1;
+  __syncthreads();
+  // the first chunk whose running sum passes x, or reaches the whole
+  for (int c = tid; c < chunks; c += kBlock)
+    if (over ? sm.front[c] >= whole : sm.front[c] > x) {
+      atomicMin(&sm.found_chunk, c);
+      break;
     }
-    front += s;
-  }
-  const bool over = c == chunks;  // x is not below the whole mass
-  if (over) {
-    c = last;
-    front = last_front;
-  }
+  __syncthreads();
+  const int c = sm.found_chunk;
+  *mine = c >= int(int64_t(chunks) * share / a.spread) &&
+          c < int(int64_t(chunks) * (share + 1) / a.spread);
+  if (!*mine) return -1;
   double v[kVec];
   const int64_t v0 = int64_t(c) * kChunk + tid * kVec;
-  weigh<DT, VEC>(w, sm.tok, v0, V, v);
+  weigh<DT, VEC>(w, sm.tok, v0, a.V, v);
   double s = 0.0;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) s += v[i];
@@ -218,7 +308,7 @@ __device__ int32_t pick(const Weights& w, double x, int64_t V, Shared& sm) {
   if (lane == kWave - 1) sm.wave[0][wv] = incl;
   if (tid == 0) sm.found = over ? -1 : INT_MAX;
   __syncthreads();
-  double at = front;
+  double at = c > 0 ? sm.front[c - 1] : 0.0;
   for (int k = 0; k < wv; ++k) at += sm.wave[0][k];
   const double before = __shfl_up(incl, 1);
   at += lane ? before : 0.0;
@@ -254,13 +344,14 @@ __device__ int32_t pick(const Weights& w, double x, int64_t V, Shared& sm) {
   return got;
 }
 
-// One workgroup per request: the walk is uniform over the workgroup (every
-// thread runs it on the same values from LDS), the passes use all of it.
+// a.spread workgroups per request. The walk is uniform over a workgroup, and the
+// same in all of a request's: every thread runs it on the same values.
 template <int DT, bool VEC>
 __global__ __launch_bounds__(kBlock) void verify_kernel(VerifyArgs a) {
   __shared__ Shared sm;
-  const int64_t b = blockIdx.x;
-  const int tid = int(threadIdx.x);
+  const int64_t b = int64_t(blockIdx.x) / a.spread;
+  const int share = int(int64_t(blockIdx.x) - b * a.spread);
+  const int tid = int(threadIdx.x), lane = tid % kWave;
   const Nodes nd = nodes_of(a.node_start, b, a.T, a.max_nodes);
   const int n = nd.n < 0 ? 0 : nd.n;
   int bits = nd.n < 0 ? SV_ERR_TREE : 0;
@@ -271,103 +362,127 @@ __global__ __launch_bounds__(kBlock) void verify_kernel(VerifyArgs a) {
   if (tid < n) {
     const int64_t i = nd.first + tid;
     const int32_t up = a.parents[i];
+    const int32_t x = a.tokens[i];
+    sm.u[tid] = a.u[i];
     wrong = tid == 0 ? up != -1 : (up < 0 || up >= tid);
     sm.up[tid] = wrong ? -1 : up;
-    const int32_t x = a.tokens[i];
     sm.tok[tid] = x;
-    sm.u[tid] = a.u[i];
     const bool fits = tid > 0 && !wrong && x >= 0 && x < a.V;
     sm.px[tid] = fits ? load_one<DT>(row_at<DT>(a.p, a.ps, nd.first + up), x) : 0.0;
     sm.qx[tid] = fits && a.q ? load_one<DT>(row_at<DT>(a.q, a.qs, nd.first + up), x) : 1.0;
   }
+  const double r = a.r[b];
   if (__syncthreads_or(wrong)) bits |= SV_ERR_TREE;
 
-  int32_t* path = a.path + b * a.max_path;
-  int32_t* emitted = a.emitted ? a.emitted + b * a.max_path : nullptr;
+  // The accepted path is kept by the lanes of wavefront 0: lane l has nodes l and
+  // l + 64 of it.
+  int32_t step0 = 0, step1 = 0;
   int taken = 0;
   int32_t y = -1;
-  const double r = a.r[b];
+  bool mine = share == 0;  // who writes: the owner of the drawn id's chunk, or the first
   if (n > 0 && bits == 0 && !(r >= 0.0 && r < 1.0)) bits |= SV_ERR_UNIFORM;
   if (n > 0 && bits == 0) {
+    const int up0 = lane < n ? sm.up[lane] : -2, up1 = 64 + lane < n ? sm.up[64 + lane] : -2;
+    const int tok0 = lane < n ? sm.tok[lane] : -1, tok1 = 64 + lane < n ? sm.tok[64 + lane] : -1;
+    uint64_t* sums = a.sums + b * (a.max_nodes + 1) * int64_t(a.chunks);
     int cur = 0;
+    uint64_t kids0 = __ballot(up0 == 0), kids1 = __ballot(up1 == 0);
     double mass = 1.0, left = 1.0;
     Weights w{row_at<DT>(a.p, a.ps, nd.first), nullptr, 0.0, 0, 0};
-    bool summed = false;  // sm.chunk holds the sums of w
-    for (int i = 1; i < n && bits == 0; ++i) {
-      if (sm.up[i] != cur) continue;
-      const int32_t x = sm.tok[i];
-      const double u = sm.u[i], px = sm.px[i], qx = sm.qx[i];
-      if (x < 0 || x >= a.V) bits |= SV_ERR_TOKEN;
-      if (!(u >= 0.0 && u < 1.0)) bits |= SV_ERR_UNIFORM;
-      if (!(px >= 0.0 && px < INFINITY && qx >= 0.0 && qx < INFINITY)) bits |= SV_ERR_ROW;
-      if (bits) break;
-      double wx, qk;
-      if (a.mode == SV_DRAFT_FIXED) {
-        wx = px;
-        for (int o = cur + 1; o < i; ++o)
-          if (sm.up[o] == cur && sm.tok[o] == x) wx = 0.0;  // rejected before
-        qk = 1.0;
-      } else {
-        const double d = fma(-w.a, qx, px);
-        wx = d > 0.0 ? d : 0.0;
-        qk = left > 0.0 ? qx / left : 0.0;
+    bool summed = false;  // sm.front holds the sums of w
+    // Walk to the next rejection or the end, take the sums that it needs, go on.
+    while (true) {
+      bool rejected = false;
+      while ((kids0 | kids1) && !rejected) {
+        const int i = kids0 ? __builtin_ctzll(kids0) : 64 + __builtin_ctzll(kids1);
+        if (kids0) kids0 &= kids0 - 1;
+        else kids1 &= kids1 - 1;
+        const int32_t x = sm.tok[i];
+        const double u = sm.u[i], px = sm.px[i], qx = sm.qx[i];
+        if (x < 0 || x >= a.V) bits |= SV_ERR_TOKEN;
+        if (!(u >= 0.0 && u < 1.0)) bits |= SV_ERR_UNIFORM;
+        if (!(px >= 0.0 && px < INFINITY && qx >= 0.0 && qx < INFINITY)) bits |= SV_ERR_ROW;
+        if (bits) break;
+        double wx, qk;
+        if (a.mode == SV_DRAFT_FIXED) {
+          // zero if it was rejected before
+          wx = (__ballot(tok0 == x) & w.gone0) | (__ballot(tok1 == x) & w.gone1) ? 0.0 : px;
+          qk = 1.0;
+        } else {
+          const double d = fma(-w.a, qx, px);
+          wx = d > 0.0 ? d : 0.0;
+          qk = left > 0.0 ? qx / left : 0.0;
+        }
+        if (u * qk * mass < wx) {
+          if (taken + 1 >= a.max_path) {
+            bits |= SV_ERR_TREE;
+            break;
+          }
+          ++taken;
+          if (lane == (taken & 63)) (taken < 64 ? step0 : step1) = i;
+          cur = i;
+          kids0 = __ballot(up0 == cur);
+          kids1 = __ballot(up1 == cur);
+          mass = left = 1.0;
+          w = Weights{row_at<DT>(a.p, a.ps, nd.first + cur), nullptr, 0.0, 0, 0};
+          summed = false;
+        } else if (a.mode == SV_DRAFT_FIXED) {
+          mass -= wx;
+          if (i < 64) w.gone0 |= uint64_t(1) << i;
+          else w.gone1 |= uint64_t(1) << (i - 64);
+        } else if (mass > 0.0 || !summed) {
+          w.q = row_at<DT>(a.q, a.qs, nd.first + cur);
+          w.a += left > 0.0 ? mass / left : 0.0;
+          if (a.mode == SV_DRAFT_DISTINCT) left -= qx;
+          rejected = true;
+        }
       }
-      if (u * qk * mass < wx) {
-        if (taken + 1 >= a.max_path) {
-          bits |= SV_ERR_TREE;
+      if (bits) break;
+      if (!rejected && summed) {
+        if (mass > 0.0) break;
+        if (!w.q && !w.gone0 && !w.gone1) {
+          bits |= SV_ERR_ROW;
           break;
         }
-        ++taken;
-        if (tid == 0) {
-          path[taken] = i;
-          if (emitted) emitted[taken - 1] = x;
-        }
-        cur = i;
-        mass = left = 1.0;
-        w = Weights{row_at<DT>(a.p, a.ps, nd.first + cur), nullptr, 0.0, 0, 0};
-        summed = false;
-      } else if (a.mode == SV_DRAFT_FIXED) {
-        mass -= wx;
-        if (i < 64) w.gone0 |= uint64_t(1) << i;
-        else w.gone1 |= uint64_t(1) << (i - 64);
-      } else if (mass > 0.0 || !summed) {
-        w.q = row_at<DT>(a.q, a.qs, nd.first + cur);
-        w.a += left > 0.0 ? mass / left : 0.0;
-        bool ok;
-        mass = mass_of<DT, VEC>(w, a.V, sm, &ok);
-        summed = true;
-        if (!ok) bits |= SV_ERR_ROW;
-        if (a.mode == SV_DRAFT_DISTINCT) left -= qx;
-      }
-    }
-    if (bits == 0) {
-      bool ok = true;
-      double total = mass;
-      if (!summed) total = mass_of<DT, VEC>(w, a.V, sm, &ok);
-      if (ok && !(total > 0.0) && (w.q || w.gone0 || w.gone1)) {
         // nothing left by rounding: from the target's row itself
         w = Weights{w.p, nullptr, 0.0, 0, 0};
-        total = mass_of<DT, VEC>(w, a.V, sm, &ok);
       }
-      if (!ok || !(total > 0.0)) bits |= SV_ERR_ROW;
-      else y = pick<DT, VEC>(w, r * total, a.V, sm);
+      mass = mass_of<DT, VEC>(a, w, sums, share, sm);
+      sums += a.chunks;
+      summed = true;
+      if (mass != mass) {
+        bits |= SV_ERR_ROW;
+        break;
+      }
     }
+    if (bits == 0) y = pick<DT, VEC>(a, w, r * mass, share, sm, &mine);
   }
   const bool none = n == 0 || bits != 0;
-  __syncthreads();
-  for (int i = tid; i < a.max_path; i += kBlock) {
-    if (none || i > taken) path[i] = -1;
-    if (emitted && (none || i > taken)) emitted[i] = -1;
+  if (!mine || tid >= kWave) return;
+  int32_t* path = a.path + b * a.max_path;
+  int32_t* emitted = a.emitted ? a.emitted + b * a.max_path : nullptr;
+  for (int i = lane; i < a.max_path; i += kWave) {
+    const bool on = !none && i <= taken;
+    path[i] = on ? (i < 64 ? step0 : step1) : -1;
+    if (emitted && !(on && i < taken)) emitted[i] = on ? y : -1;
+    if (emitted && on && i > 0) emitted[i - 1] = sm.tok[i < 64 ? step0 : step1];
   }
-  if (tid == 0) {
-    if (!none) {
-      path[0] = 0;
-      if (emitted) emitted[taken] = y;
-    }
+  if (lane == 0) {
     a.accept_len[b] = none ? -1 : taken;
     a.out_token[b] = none ? -1 : y;
     if (bits) set_error(a.err, bits);
   }
+}
+
+__global__ __launch_bounds__(256) void clear_kernel(uint64_t* x, int64_t n) {
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n; i += int64_t(gridDim.x) * 256)
+    x[i] = kEmpty;
+}
+
+// Workgroups of a request: enough to fill the card, each with a chunk at least.
+int spread_of(int64_t B, int64_t chunks) {
+  const int64_t most = kWorkers / B;
+  return int(most < 1 ? 1 : most < chunks ? most : chunks);
 }
 
 bool sizes_ok(int64_t B, int64_t V, int64_t max_nodes) {
@@ -380,7 +495,10 @@ bool sizes_ok(int64_t B, int64_t V, int64_t max_nodes) {
 extern "C" {
 
 size_t specverify_tree_verify_workspace_size(int64_t B, int64_t V, int64_t max_nodes) {
-  return sizes_ok(B, V, max_nodes) ? 256 : 0;
+  if (!sizes_ok(B, V, max_nodes)) return 0;
+  const int64_t chunks = (V + kChunk - 1) / kChunk;
+  if (spread_of(B, chunks) == 1) return 256;
+  return align256(size_t(B) * size_t(max_nodes + 1) * size_t(chunks) * 8);
 }
 
 int specverify_tree_verify(const void* target_probs, const void* draft_probs, int dtype, int mode,
@@ -406,11 +524,20 @@ int specverify_tree_verify(const void* target_probs, const void* draft_probs, in
   const int esz = dtype == SV_BF16 ? 2 : 4;
   const bool vec = aligned16(target_probs) && aligned16(draft_probs) &&
                    t_stride * esz % 16 == 0 && d_stride * esz % 16 == 0;
+  const int64_t chunks = (V + kChunk - 1) / kChunk;
+  const int spread = spread_of(B, chunks);
+  if (B * spread >= (int64_t(1) << 31)) return SV_EINVAL;
+  uint64_t* sums = static_cast<uint64_t*>(workspace);
   VerifyArgs a{target_probs, draft_probs, t_stride, d_stride, tokens, parents, node_start, u, r, T,
-               V, int(max_nodes), int(max_path), mode, accept_len, path, emitted, out_token,
-               device_error};
+               V, int(max_nodes), int(max_path), mode, spread, int(chunks), sums, accept_len, path,
+               emitted, out_token, device_error};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const dim3 grid{unsigned(B)}, block{kBlock};
+  if (spread > 1) {
+    const int64_t words = B * (max_nodes + 1) * chunks, blocks = (words + 1023) / 1024;
+    hipLaunchKernelGGL(clear_kernel, dim3(unsigned(blocks < 2048 ? blocks : 2048)), dim3(256), 0, s,
+                       sums, words);
+  }
+  const dim3 grid{unsigned(B * spread)}, block{kBlock};
   if (dtype == SV_BF16) {
     if (vec) hipLaunchKernelGGL((verify_kernel<SV_BF16, true>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((verify_kernel<SV_BF16, false>), grid, block, 0, s, a);
