@@ -73,7 +73,7 @@ struct AttnArgs {
   // workspace
   struct Split* split;  // [workers], and all tiles in one more's start
   float* part;          // [workers * 2][M][DP + 4]: sums, then m and l
-  int tile_keys, tile_rows, width;
+  int tile_keys, tile_rows, width, whole;
 };
 
 // An item (request, key head, row tile) that a worker began inside of: its tiles
@@ -134,9 +134,15 @@ __device__ __forceinline__ Req uniform_request(Args a, int64_t b) {
 // Work is shared out in places: an item (request, key head, row tile) takes one
 // for each of its tiles and kItemPlaces more for what it costs besides (rows
 // loaded, wavefronts joined, results written).
+// Where no request can have many tiles, items are not split (`whole`): one place
+// each, and nothing to join.
 constexpr int kItemPlaces = 3;
-__device__ __forceinline__ int64_t places_of(int heads, const Req& r) {
-  return int64_t(r.tiles + kItemPlaces) * r.row_tiles * heads;
+constexpr int kWholeTiles = 6;
+__device__ __forceinline__ int item_places(int whole, int tiles) {
+  return whole ? 1 : tiles + kItemPlaces;
+}
+__device__ __forceinline__ int64_t places_of(int whole, int heads, const Req& r) {
+  return int64_t(item_places(whole, r.tiles)) * r.row_tiles * heads;
 }
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -244,7 +250,6 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   __shared__ __align__(1024) char tile[S * STAGE];
   __shared__ float merge_ml[KW][RW][2][32];
   __shared__ int64_t scan[NT / 64];
-  __shared__ int64_t found[2];
   __shared__ Seg segs[S + 2];
   __shared__ Cursor cursors[2];
   __shared__ int32_t id_box[NT / 64][2][64];
@@ -265,9 +270,11 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   }
   // All tiles, and those in front of this thread's request (of the last round).
   int64_t total = 0, mine = 0, lo = 0;
+  Req own{};
   for (int64_t o = 0; o < a.B; o += NT) {
     int bits = 0;
-    mine = o + tid < a.B ? places_of(a.Hkv, request(a, o + tid, &bits)) : 0;
+    if (o + tid < a.B) own = request(a, o + tid, &bits);
+    mine = o + tid < a.B ? places_of(a.whole, a.Hkv, own) : 0;
     if (w == 0 && bits) set_error(a.err, bits);
     int64_t s = mine;
     for (int d = 1; d < 64; d *= 2) {
@@ -291,7 +298,8 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   int64_t base = 0;
   for (int64_t o = 0; o < a.B; o += NT) {
     if (a.B > NT) {
-      mine = o + tid < a.B ? places_of(a.Hkv, request(a, o + tid)) : 0;
+      if (o + tid < a.B) own = request(a, o + tid);
+      mine = o + tid < a.B ? places_of(a.whole, a.Hkv, own) : 0;
       int64_t s = mine;
       for (int d = 1; d < 64; d *= 2) {
         const int64_t y = __shfl_up(s, d);
@@ -306,16 +314,8 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
         base += scan[k];
       }
     }
-    if (at >= lo && at < lo + mine) {
-      found[0] = o + tid;
-      found[1] = lo;
-    }
+    if (at >= lo && at < lo + mine) cursors[0] = Cursor{at, o + tid, lo, own};
     if (base > at) break;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    const int64_t b = found[0];
-    cursors[0] = Cursor{at, b, found[1], request(a, b)};
   }
   __syncthreads();
 
@@ -379,18 +379,18 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
         more = false;
         return;
       }
-      while (at >= b_first + places_of(s->Hkv, rq)) {
-        b_first += places_of(s->Hkv, rq);
+      while (at >= b_first + places_of(s->whole, s->Hkv, rq)) {
+        b_first += places_of(s->whole, s->Hkv, rq);
         rq = uniform_request(s, ++b);
       }
       const int64_t into = at - b_first;
-      const int size = rq.tiles + kItemPlaces;
+      const int size = item_places(s->whole, rq.tiles);
       const int item = int(into / size);  // (key head, row tile)
       const int p0 = int(into - int64_t(item) * size);
       const int p1 = int(size - p0 < end - at ? size : p0 + (end - at));
       sg.start = at - p0;
       sg.t0 = min(p0, rq.tiles);
-      sg.t1 = min(p1, rq.tiles);
+      sg.t1 = s->whole ? rq.tiles : min(p1, rq.tiles);
       sg.h = item / rq.row_tiles;
       sg.rt = item - sg.h * rq.row_tiles;
       at += p1 - p0;
@@ -549,10 +549,10 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   };
 
   prepare();
-  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
   meet();
   if (more) load_rows(0);
   rows_here();
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");  // the first page ids
   int fetched = 0, done = 0;
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) {
@@ -718,57 +718,58 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
       l += __shfl_xor(l, 32);
 
       if constexpr (KW > 1) {
-        // The wavefronts along the keys join in this tile's stage, JOIN blocks of
-        // columns at a time; the other stages are being filled.
+        // The wavefronts along the keys join in this tile's stage (the others are
+        // being filled), JOIN blocks of columns at a time; each adds up the blocks
+        // i with i % KW = kw, and writes those out.
         if (half == 0) {
           merge_ml[kw][rw][0][col] = m;
           merge_ml[kw][rw][1][col] = l;
         }
-        float* const box = reinterpret_cast<float*>(tile + st_now * STAGE);
-        float ref = 0.0f, f[KW];
+        float* const box = reinterpret_cast<float*>(tile + st_now * STAGE) + lane;
+        float mine = 1.0f, f[KW];
 #pragma unroll
         for (int i0 = 0; i0 < ND; i0 += JOIN) {
           meet();
-          if (kw > 0) {
-            float* o = box + ((kw - 1) * RW + rw) * (JOIN * 16 * 64);
+          if (i0 == 0) {
+            float to = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < JOIN; ++i)
+            for (int k = 0; k < KW; ++k) to = fmaxf(to, merge_ml[k][rw][0][col]);
+            const float ref = to == -INFINITY ? 0.0f : to;
+            mine = __builtin_amdgcn_exp2f(m - ref);
+            l = 0.0f;
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[(i * 16 + j) * 64 + lane] = acc[i0 + i][j];
+            for (int k = 0; k < KW; ++k) {
+              f[k] = __builtin_amdgcn_exp2f(merge_ml[k][rw][0][col] - ref);
+              l = fmaf(f[k], merge_ml[k][rw][1][col], l);
+            }
+            m = to;
+          }
+#pragma unroll
+          for (int i = 0; i < JOIN; ++i) {
+            const int owner = (i0 + i) % KW;
+            if (kw == owner) continue;
+            float* o = box + ((i * (KW - 1) + (kw < owner ? kw : kw - 1)) * RW + rw) * (16 * 64);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j * 64] = acc[i0 + i][j];
           }
           meet();
-          if (kw == 0) {
-            if (i0 == 0) {
-              float to = m;
 #pragma unroll
-              for (int k = 1; k < KW; ++k) to = fmaxf(to, merge_ml[k][rw][0][col]);
-              ref = to == -INFINITY ? 0.0f : to;
-              f[0] = __builtin_amdgcn_exp2f(m - ref);
-              l *= f[0];
+          for (int i = 0; i < JOIN; ++i) {
+            const int owner = (i0 + i) % KW;
+            if (kw != owner) continue;
+            acc[i0 + i] *= mine;
 #pragma unroll
-              for (int k = 1; k < KW; ++k) {
-                f[k] = __builtin_amdgcn_exp2f(merge_ml[k][rw][0][col] - ref);
-                l += f[k] * merge_ml[k][rw][1][col];
-              }
-              m = to;
-            }
+            for (int k = 0; k < KW; ++k) {
+              if (k == owner) continue;
+              const float* o = box + ((i * (KW - 1) + (k < owner ? k : k - 1)) * RW + rw) * (16 * 64);
 #pragma unroll
-            for (int i = 0; i < JOIN; ++i) {
-              acc[i0 + i] *= f[0];
-#pragma unroll
-              for (int k = 1; k < KW; ++k) {
-                const float* o = box + ((k - 1) * RW + rw) * (JOIN * 16 * 64);
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  acc[i0 + i][j] = fmaf(f[k], o[(i * 16 + j) * 64 + lane], acc[i0 + i][j]);
-              }
-              __builtin_amdgcn_sched_barrier(0);  // few registers rather than many reads at once
+              for (int j = 0; j < 16; ++j) acc[i0 + i][j] = fmaf(f[k], o[j * 64], acc[i0 + i][j]);
             }
           }
         }
       }
 
-      if (wild && kw == 0) {
+      if (wild) {
         // The wild values of the nodes among this share's keys, for the rows that
         // see them (rare, so scores are simply taken again).
         for (int x = max(t0 * KT - len, 0); x < min(t1 * KT - len, n); ++x) {
@@ -797,12 +798,13 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
       }
 
       rows_here();
-      if (kw == 0 && row_ok) {
+      if (row_ok) {
         if (whole) {
           const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
           char* op = s->out + (first + node) * s->o_t + hq * s->o_h;
 #pragma unroll
-          for (int i = 0; i < ND; ++i)
+          for (int i = 0; i < ND; ++i) {
+            if (i % KW != kw) continue;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int d = i * 32 + 8 * j + 4 * half;
@@ -814,7 +816,8 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
                 *reinterpret_cast<e4*>(op + d * 2) = x;
               }
             }
-          if (s->lse && half == 0)
+          }
+          if (s->lse && half == 0 && kw == 0)
             s->lse[(first + node) * s->Hq + hq] =
                 l > 0.0f || l != l ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
         } else {
@@ -822,12 +825,14 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
           // item (its first), slot 1 if it ends inside (its last)
           float* p = s->part + ((w * 2 + (t0 > 0 ? 0 : 1)) * M + rw * 32 + col) * int64_t(DP + 4);
 #pragma unroll
-          for (int i = 0; i < ND; ++i)
+          for (int i = 0; i < ND; ++i) {
+            if (i % KW != kw) continue;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               *reinterpret_cast<f32x4*>(p + i * 32 + 8 * j + 4 * half) =
                   f32x4{acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]};
-          if (half == 0) {
+          }
+          if (half == 0 && kw == 0) {
             p[DP] = m;
             p[DP + 1] = l;
           }
@@ -929,19 +934,19 @@ void launch(const Variant& v, const AttnArgs& a, hipStream_t st) {
   }
 }
 
+template <int DT, int DP>
+void launch_both(const Variant& v, const AttnArgs& a, hipStream_t st) {
+  launch<DT, DP>(v, a, st);
+  if (a.whole) return;
+  const dim3 grid{unsigned(v.workers), unsigned(32 * v.rw * DP / 1024)};
+  hipLaunchKernelGGL((join_kernel<DT, DP>), grid, dim3(256), 0, st, a, v.workers);
+}
+
 template <int DT>
 void launch_width(const Variant& v, const AttnArgs& a, hipStream_t st) {
-  const dim3 grid{unsigned(v.workers), unsigned(32 * v.rw * v.width / 1024)};
-  if (v.width == 64) {
-    launch<DT, 64>(v, a, st);
-    hipLaunchKernelGGL((join_kernel<DT, 64>), grid, dim3(256), 0, st, a, v.workers);
-  } else if (v.width == 128) {
-    launch<DT, 128>(v, a, st);
-    hipLaunchKernelGGL((join_kernel<DT, 128>), grid, dim3(256), 0, st, a, v.workers);
-  } else {
-    launch<DT, 256>(v, a, st);
-    hipLaunchKernelGGL((join_kernel<DT, 256>), grid, dim3(256), 0, st, a, v.workers);
-  }
+  if (v.width == 64) launch_both<DT, 64>(v, a, st);
+  else if (v.width == 128) launch_both<DT, 128>(v, a, st);
+  else launch_both<DT, 256>(v, a, st);
 }
 
 bool sizes_ok(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_nodes) {
@@ -1040,6 +1045,7 @@ int specverify_tree_attention(
   a.tile_keys = v.kw * v.kb;
   a.tile_rows = 32 * v.rw;
   a.width = v.width;
+  a.whole = max_pages * page_size + max_nodes <= kWholeTiles * int64_t(a.tile_keys) ? 1 : 0;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (dtype == SV_BF16) launch_width<SV_BF16>(v, a, st);
   else launch_width<SV_F16>(v, a, st);
