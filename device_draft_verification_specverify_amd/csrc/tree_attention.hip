@@ -134,8 +134,10 @@ __device__ __forceinline__ Req uniform_request(Args a, int64_t b) {
 // Work is shared out in places: an item (request, key head, row tile) takes one
 // for each of its tiles and kItemPlaces more for what it costs besides (rows
 // loaded, wavefronts joined, results written).
-// Where no request can have many tiles, items are not split (`whole`): one place
-// each, and nothing to join.
+// Where no request can have many tiles and every item has a worker, items are not
+// split (`whole`): one place each, and nothing to join (32 requests of up to 600
+// tokens: 25 us so, 30 us split; 256 requests, with 8 items a worker, 170 us so,
+// 147 us split).
 constexpr int kItemPlaces = 3;
 constexpr int kWholeTiles = 6;
 __device__ __forceinline__ int item_places(int whole, int tiles) {
@@ -525,9 +527,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
 #pragma unroll
     for (int k = 0; k < DP / 16; ++k) {
       const int d = 16 * k + 8 * half;
-      u32x4 x = {0, 0, 0, 0};
-      if (d < s->D) x = *reinterpret_cast<const u32x4*>(qp + d * 2);
-      qf[k] = x;
+      qf[k] = *reinterpret_cast<const u32x4*>(d < s->D ? qp + d * 2 : zero);
     }
     if (s->anc) {
       const uint64_t* words = s->anc + i * s->words;
@@ -801,20 +801,18 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
       if (row_ok) {
         if (whole) {
           const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-          char* op = s->out + (first + node) * s->o_t + hq * s->o_h;
+          char* op = s->out + (first + node) * s->o_t + hq * s->o_h + 8 * half;
 #pragma unroll
           for (int i = 0; i < ND; ++i) {
             if (i % KW != kw) continue;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const int d = i * 32 + 8 * j + 4 * half;
-              if (d < s->D) {
-                typedef elem e4 __attribute__((ext_vector_type(4)));
-                e4 x;
+              if (i * 32 + 8 * j >= s->D) continue;  // D is a multiple of 8
+              typedef elem e4 __attribute__((ext_vector_type(4)));
+              e4 x;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] = elem(acc[i][4 * j + k] * inv);
-                *reinterpret_cast<e4*>(op + d * 2) = x;
-              }
+              for (int k = 0; k < 4; ++k) x[k] = elem(acc[i][4 * j + k] * inv);
+              *reinterpret_cast<e4*>(op + (i * 32 + 8 * j) * 2) = x;
             }
           }
           if (s->lse && half == 0 && kw == 0)
@@ -1045,7 +1043,9 @@ int specverify_tree_attention(
   a.tile_keys = v.kw * v.kb;
   a.tile_rows = 32 * v.rw;
   a.width = v.width;
-  a.whole = max_pages * page_size + max_nodes <= kWholeTiles * int64_t(a.tile_keys) ? 1 : 0;
+  const int64_t items = B * Hkv * ((max_nodes * (Hq / Hkv) + a.tile_rows - 1) / a.tile_rows);
+  a.whole = max_pages * page_size + max_nodes <= kWholeTiles * int64_t(a.tile_keys) &&
+            items <= v.workers;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (dtype == SV_BF16) launch_width<SV_BF16>(v, a, st);
   else launch_width<SV_F16>(v, a, st);
