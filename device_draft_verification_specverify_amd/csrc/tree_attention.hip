@@ -105,10 +105,10 @@ __device__ __forceinline__ Req request(const AttnArgs& a, int64_t b, int* bits =
 }
 // The kernel's arguments where they are seldom used: read again at each such
 // place, or some hundred of them would be held in scalar registers throughout
-// and push out what the loop over the tiles uses.
+// and push out what the loop over the tiles uses. (The pointer to them is taken
+// once, in the kernel: elsewhere there is none.)
 typedef const __attribute__((address_space(4))) AttnArgs* Args;
-__device__ __forceinline__ Args seldom() {
-  Args p = (Args)__builtin_amdgcn_kernarg_segment_ptr();
+__device__ __forceinline__ Args again(Args p) {
   asm volatile("" : "+s"(p));
   return p;
 }
@@ -189,14 +189,14 @@ __device__ __forceinline__ uint64_t window(uint64_t m0, uint64_t m1, int x) {
 __device__ __forceinline__ void load_lds16(const char* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
-               : "s"(to), "v"(from)
+               : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(from)
                : "memory", "m0");
 }
 
 __device__ __forceinline__ void load_lds4(const int32_t* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                :
-               : "s"(to), "v"(from)
+               : "s"(__builtin_amdgcn_readfirstlane(to)), "v"(from)
                : "memory", "m0");
 }
 
@@ -256,6 +256,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   __shared__ Cursor cursors[2];
   __shared__ int32_t id_box[NT / 64][2][64];
   __shared__ int wild_seg;
+  const Args args = (Args)__builtin_amdgcn_kernarg_segment_ptr();
   const int tid = int(threadIdx.x), lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rw = wv % RW, kw = wv / RW;
@@ -292,8 +293,8 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
       total += scan[k];
     }
   }
-  int64_t at = share_start(total, workers, w);
-  const int64_t end = share_start(total, workers, w + 1);
+  const int64_t at = uniform(share_start(total, workers, w));
+  const int64_t end = uniform(share_start(total, workers, w + 1));
   if (w == 0 && tid == 0) a.split[workers].start = total;
   if (at >= end) return;
   // the request that holds tile `at`: more than NT of them are gone through again
@@ -359,18 +360,18 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   const uint32_t id_at = uniform(int(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) char*)&id_box[wv][0][0])));
   // this lane's page id in the batch of tiles from t on (the prefix's last at most)
-  auto id_place = [&](const int32_t* table, int t, int len) {
+  auto id_place = [&](const int32_t* table, int t, int len) __attribute__((always_inline)) {
     const int key = (t + lane / UNITS) * KT + lane % UNITS * (NT / CPR) + wv * WROWS;
     return table + ((key < len ? key : len - 1) >> page_shift);
   };
-  auto take_ids = [&](int box) {
+  auto take_ids = [&](int box) __attribute__((always_inline)) {
     ids = id_box[wv][box][lane];
     asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(ids) : : "memory");
   };
 
   // Finds the next share of this worker, with its first page ids on their way.
-  auto prepare = [&]() {
-    const Args s = seldom();
+  auto prepare = [&]() __attribute__((always_inline)) {
+    const Args s = again(args);
     const Cursor& cursor = cursors[turn];
     int64_t at = uniform(cursor.at), b = uniform(cursor.b), b_first = uniform(cursor.b_first);
     Req rq{uniform(cursor.rq.first), uniform(cursor.rq.n), uniform(cursor.rq.len),
@@ -415,7 +416,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   };
   // Starts the next tile's keys and values on their way into a stage; false when
   // the share is at its end.
-  auto fetch_next = [&](int to_stage) {
+  auto fetch_next = [&](int to_stage) __attribute__((always_inline)) {
     const bool fresh = f_t == f_t1;
     if (fresh) {
       if (!more) return false;
@@ -473,7 +474,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
     } else {
       // the end of the prefix, the tree's nodes, pages of fewer rows than a
       // wavefront loads, bad pages: lane by lane
-      const Args s = seldom();
+      const Args s = again(args);
       int32_t page[UNITS];
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) {
@@ -515,8 +516,8 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
 
   // The rows of share `which`: this lane's part of them to registers, and its mask.
   uint64_t next_see0 = 0, next_see1 = 0;
-  auto load_rows = [&](int which) {
-    const Args s = seldom();
+  auto load_rows = [&](int which) __attribute__((always_inline)) {
+    const Args s = again(args);
     const Seg& sg = segs[which % (S + 2)];
     const int n = uniform(sg.n), h = uniform(sg.h), row0 = uniform(sg.rt) * M + rw * 32;
     if (row0 >= n * s->G) return;
@@ -542,7 +543,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   // They are asked for when a share ends, and here before its results are
   // written: where the loop over tiles began with them on their way, the
   // compiler would wait for every load in it.
-  auto rows_here = [&]() {
+  auto rows_here = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int k = 0; k < DP / 16; ++k) asm volatile("" : "+v"(qf[k]));
     asm volatile("" : "+v"(next_see0), "+v"(next_see1));
@@ -567,7 +568,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
     else wait_and_meet<0>();
 
     if (t == t1) {
-      const Args s = seldom();
+      const Args s = again(args);
       const Seg& sg = segs[seg % (S + 2)];
       t = uniform(sg.t0);
       t1 = uniform(sg.t1);
@@ -643,7 +644,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
       // V^T of a half block of keys: columns d of this lane, keys in the order
       // of the scores
       s16x8 vf[2][STEP / 2];
-      auto read_v = [&](int half_block, int db0, s16x8* to) {
+      auto read_v = [&](int half_block, int db0, s16x8* to) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < STEP / 2; ++i) {
           const uint32_t at = (stage + v_off) ^ ((db0 + i) * 64);
@@ -710,7 +711,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
     ++t;
     if (t == t1) {
       if (fetched - done > 1) load_rows(seg);
-      const Args s = seldom();
+      const Args s = again(args);
       const Seg& sg = segs[(seg - 1) % (S + 2)];
       const int t0 = uniform(sg.t0), h = uniform(sg.h);
       const int64_t first = uniform(sg.first);
