@@ -982,7 +982,7 @@ int specverify_tree_attention(
   if (!sizes_ok(B, T, Hq, Hkv, D, max_nodes)) return SV_EINVAL;
   const int64_t k31 = int64_t(1) << 31;
   if (!pow2(page_size) || page_size >= k31 || max_pages < 1 || max_pages >= k31 ||
-      max_pages * page_size + max_nodes > k31 - (1 << 12) || num_pages < 1 || num_pages >= k31 ||
+      max_pages * page_size + max_nodes > k31 - (1 << 14) || num_pages < 1 || num_pages >= k31 ||
       table_stride < max_pages)
     return SV_EINVAL;
   const int64_t strides[] = {q_stride_t, q_stride_h, n_stride_t, n_stride_h, c_stride_page,

@@ -11,6 +11,12 @@
 // w_k(x) <= u S_k q(x) / Q_k < (S_k / Q_k) q(x), so its w is zero from then on.
 // Accept tests read two scalars of each row, so only rejections and the last
 // node cost a pass.
+//
+// What bounds it is the chain of those passes: one is 1 MB of two float32 rows at
+// V = 128256, about 4 us with its sums gathered from 8 workgroups, and none can
+// begin before the one before has decided. 64 chains of 9 nodes (one or two
+// passes each, 66 MB of rows) take 24 us; 24 trees of 33 nodes 36 us; one chain
+// at V = 32000 13 us, most of it trips to memory that wait for each other.
 
 #include "tree_common.h"
 
@@ -121,27 +127,34 @@ struct Weights {
 
 __device__ __forceinline__ bool proper(float x) { return x >= 0.0f && x < INFINITY; }
 
-// The weights of ids v0 .. v0 + 7; false if a probability among them is none.
+// Target and draft probabilities of ids v0 .. v0 + 7.
+struct Probs {
+  float p[kVec], q[kVec];
+};
+
 template <int DT, bool VEC>
-__device__ __forceinline__ bool weigh(const Weights& w, const int32_t* tok, int64_t v0, int64_t V,
-                                      double (&x)[kVec]) {
-  float p[kVec];
-  load8<DT, VEC>(w.p, v0, V, p);
+__device__ __forceinline__ void read_probs(const void* p, const void* q, int64_t v0, int64_t V,
+                                           Probs& r) {
+  load8<DT, VEC>(p, v0, V, r.p);
+  if (q) load8<DT, VEC>(q, v0, V, r.q);
+}
+
+// The weights of these ids; false if a probability among them is none.
+__device__ __forceinline__ bool weigh(const Weights& w, const int32_t* tok, int64_t v0,
+                                      const Probs& r, double (&x)[kVec]) {
   bool ok = true;
   if (w.q) {
-    float q[kVec];
-    load8<DT, VEC>(w.q, v0, V, q);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      ok = ok && proper(p[i]) && proper(q[i]);
-      const double d = fma(-w.a, double(q[i]), double(p[i]));
+      ok = ok && proper(r.p[i]) && proper(r.q[i]);
+      const double d = fma(-w.a, double(r.q[i]), double(r.p[i]));
       x[i] = d > 0.0 ? d : 0.0;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      ok = ok && proper(p[i]);
-      x[i] = double(p[i]);
+      ok = ok && proper(r.p[i]);
+      x[i] = double(r.p[i]);
     }
     for (uint64_t g = w.gone0; g; g &= g - 1) {
       const int64_t at = int64_t(tok[__builtin_ctzll(g)]) - v0;
@@ -183,8 +196,21 @@ struct Shared {
 // bits. Several at once, because one chunk's loads are not enough in flight.
 template <bool VEC>
 constexpr int kAtOnce = VEC ? 4 : 1;
+template <bool VEC>
+struct Held {
+  Probs x[kAtOnce<VEC>];
+};
+// (behind the range: its last chunk again, not used)
 template <int DT, bool VEC>
-__device__ __forceinline__ uint64_t chunk_masses(const Weights& w, int64_t V, Shared& sm, int c,
+__device__ __forceinline__ void hold(Held<VEC>& h, const void* p, const void* q, int64_t V, int c,
+                                     int c1) {
+#pragma unroll
+  for (int u = 0; u < kAtOnce<VEC>; ++u)
+    read_probs<DT, VEC>(p, q, int64_t(c + u < c1 ? c + u : c1 - 1) * kChunk + threadIdx.x * kVec, V,
+                        h.x[u]);
+}
+template <bool VEC, typename Get>  // get(u): the probabilities of chunk c + u
+__device__ __forceinline__ uint64_t chunk_masses(const Weights& w, Get get, Shared& sm, int c,
                                                  int c1) {
   const int tid = int(threadIdx.x), lane = tid % kWave, wv = tid / kWave;
   double s[kAtOnce<VEC>];
@@ -192,9 +218,8 @@ __device__ __forceinline__ uint64_t chunk_masses(const Weights& w, int64_t V, Sh
 #pragma unroll
   for (int u = 0; u < kAtOnce<VEC>; ++u) {
     double x[kVec];
-    // (behind the range: the row's last chunk again, not used)
     const int64_t at = c + u < c1 ? c + u : c1 - 1;
-    good[u] = weigh<DT, VEC>(w, sm.tok, at * kChunk + tid * kVec, V, x);
+    good[u] = weigh(w, sm.tok, at * kChunk + tid * kVec, get(u), x);
     s[u] = 0.0;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) s[u] += x[i];
@@ -223,9 +248,15 @@ __device__ __forceinline__ uint64_t chunk_masses(const Weights& w, int64_t V, Sh
 // share of a pass's chunks and publishes their sums, which are value and flag in
 // one 64-bit word. Nothing depends on all of them being resident at once: one
 // that has waited long enough takes what is missing itself (the same bits).
-template <int DT, bool VEC>
+//
+// KEEP: a workgroup has no more chunks than it takes at once, so a node's rows stay
+// in registers for its further rejections (24 trees of 33 nodes at V = 128256: 37
+// us so, 42 us read again; reading the next child's rows ahead on top of it cost
+// 8 us, because the other workgroups' sums queue behind those loads).
+template <int DT, bool VEC, bool KEEP>
 __device__ __forceinline__ double mass_of(const VerifyArgs& a, const Weights& w, uint64_t* sums,
-                                          int share, Shared& sm) {
+                                          int share, Shared& sm, Held<VEC>& held,
+                                          bool& here) {
   const int tid = int(threadIdx.x), lane = tid % kWave;
   const int chunks = a.chunks;
   int c0 = int(int64_t(chunks) * share / a.spread);
@@ -238,7 +269,22 @@ __device__ __forceinline__ double mass_of(const VerifyArgs& a, const Weights& w,
           there = there && (uint64_t)__double_as_longlong(sm.front[u]) != kEmpty;
         if (there) continue;
       }
-      const uint64_t s = chunk_masses<DT, VEC>(w, a.V, sm, c, c1);
+      uint64_t s;
+      if constexpr (KEEP) {
+        if (!here || !own) hold<DT, VEC>(held, w.p, w.q, a.V, c, c1);
+        here = own;
+        s = chunk_masses<VEC>(w, [&](int u) -> const Probs& { return held.x[u]; }, sm, c, c1);
+      } else {
+        s = chunk_masses<VEC>(
+            w,
+            [&](int u) {
+              Probs r;
+              read_probs<DT, VEC>(w.p, w.q, int64_t(c + u < c1 ? c + u : c1 - 1) * kChunk + tid * kVec,
+                                  a.V, r);
+              return r;
+            },
+            sm, c, c1);
+      }
       if (tid < kAtOnce<VEC> && c + tid < c1) {
         sm.front[c + tid] = __longlong_as_double((long long)s);
         if (own && a.spread > 1)
@@ -279,7 +325,7 @@ __device__ __forceinline__ double mass_of(const VerifyArgs& a, const Weights& w,
 // the last one with a weight when rounding leaves none. -1 from a workgroup that
 // does not own the id's chunk.
 template <int DT, bool VEC>
-__device__ int32_t pick(const VerifyArgs& a, const Weights& w, double x, int share, Shared& sm,
+__device__ __forceinline__ int32_t pick(const VerifyArgs& a, const Weights& w, double x, int share, Shared& sm,
                         bool* mine) {
   const int tid = int(threadIdx.x), lane = tid % kWave, wv = tid / kWave;
   const int chunks = a.chunks;
@@ -300,7 +346,9 @@ __device__ int32_t pick(const VerifyArgs& a, const Weights& w, double x, int sha
   if (!*mine) return -1;
   double v[kVec];
   const int64_t v0 = int64_t(c) * kChunk + tid * kVec;
-  weigh<DT, VEC>(w, sm.tok, v0, a.V, v);
+  Probs probs;
+  read_probs<DT, VEC>(w.p, w.q, v0, a.V, probs);
+  weigh(w, sm.tok, v0, probs, v);
   double s = 0.0;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) s += v[i];
@@ -346,7 +394,7 @@ __device__ int32_t pick(const VerifyArgs& a, const Weights& w, double x, int sha
 
 // a.spread workgroups per request. The walk is uniform over a workgroup, and the
 // same in all of a request's: every thread runs it on the same values.
-template <int DT, bool VEC>
+template <int DT, bool VEC, bool KEEP>
 __global__ __launch_bounds__(kBlock) void verify_kernel(VerifyArgs a) {
   __shared__ Shared sm;
   const int64_t b = int64_t(blockIdx.x) / a.spread;
@@ -390,6 +438,8 @@ __global__ __launch_bounds__(kBlock) void verify_kernel(VerifyArgs a) {
     double mass = 1.0, left = 1.0;
     Weights w{row_at<DT>(a.p, a.ps, nd.first), nullptr, 0.0, 0, 0};
     bool summed = false;  // sm.front holds the sums of w
+    Held<VEC> held;
+    int held_node = -1;  // whose rows they are
     // Walk to the next rejection or the end, take the sums that it needs, go on.
     while (true) {
       bool rejected = false;
@@ -447,7 +497,9 @@ __global__ __launch_bounds__(kBlock) void verify_kernel(VerifyArgs a) {
         // nothing left by rounding: from the target's row itself
         w = Weights{w.p, nullptr, 0.0, 0, 0};
       }
-      mass = mass_of<DT, VEC>(a, w, sums, share, sm);
+      bool here = held_node == cur;
+      mass = mass_of<DT, VEC, KEEP>(a, w, sums, share, sm, held, here);
+      held_node = here ? cur : -1;
       sums += a.chunks;
       summed = true;
       if (mass != mass) {
@@ -480,9 +532,9 @@ __global__ __launch_bounds__(256) void clear_kernel(uint64_t* x, int64_t n) {
 }
 
 // Workgroups of a request: enough to fill the card, each with the chunks that it
-// takes at once; with fewer, the sums travel longer than they take (24 trees of
-// 33 nodes at V = 128256: 42 us so, 65 us with a chunk each, 57 us with 8; one
-// chain at V = 32000: 13 us so, 19 us with a chunk each).
+// takes at once; with fewer, the sums travel longer than they take (rows read in
+// every pass, 24 trees of 33 nodes at V = 128256: 42 us so, 65 us with a chunk
+// each, 57 us with 8; one chain at V = 32000: 13 us so, 19 us with a chunk each).
 int spread_of(int64_t B, int64_t chunks) {
   const int64_t shares = chunks / kAtOnce<true>, most = kWorkers / B;
   return int(most < 1 || shares < 1 ? 1 : most < shares ? most : shares);
@@ -541,12 +593,18 @@ int specverify_tree_verify(const void* target_probs, const void* draft_probs, in
                        sums, words);
   }
   const dim3 grid{unsigned(B * spread)}, block{kBlock};
+  // Held rows take the registers of a second workgroup on the CU: not where the
+  // grid needs it, nor for chains and given drafts, whose walks take one pass.
+  const bool keep = vec && mode != SV_DRAFT_FIXED && spread > 1 && B * spread <= kWorkers / 2 &&
+                    (chunks + spread - 1) / spread <= kAtOnce<true>;
   if (dtype == SV_BF16) {
-    if (vec) hipLaunchKernelGGL((verify_kernel<SV_BF16, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((verify_kernel<SV_BF16, false>), grid, block, 0, s, a);
+    if (keep) hipLaunchKernelGGL((verify_kernel<SV_BF16, true, true>), grid, block, 0, s, a);
+    else if (vec) hipLaunchKernelGGL((verify_kernel<SV_BF16, true, false>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((verify_kernel<SV_BF16, false, false>), grid, block, 0, s, a);
   } else {
-    if (vec) hipLaunchKernelGGL((verify_kernel<SV_F32, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((verify_kernel<SV_F32, false>), grid, block, 0, s, a);
+    if (keep) hipLaunchKernelGGL((verify_kernel<SV_F32, true, true>), grid, block, 0, s, a);
+    else if (vec) hipLaunchKernelGGL((verify_kernel<SV_F32, true, false>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((verify_kernel<SV_F32, false, false>), grid, block, 0, s, a);
   }
   return launch_status();
 }

@@ -154,7 +154,7 @@ size_t specverify_tree_attention_workspace_size(int64_t B, int64_t T, int64_t Hq
  * T = 0, the [T, ...] arrays; B, Hq, Hkv < 1, Hq not a multiple of Hkv, T < 0,
  * D no multiple of 8 or outside [8, 256], max_nodes outside [1, 128],
  * max_nodes * Hq / Hkv > 2^16, B * Hkv > 2^24, page_size no power of two,
- * max_pages < 1 or max_pages * page_size + max_nodes > 2^31 - 2^12, T * Hq >= 2^31,
+ * max_pages < 1 or max_pages * page_size + max_nodes > 2^31 - 2^14, T * Hq >= 2^31,
  * num_pages < 1, negative stride, table_stride < max_pages, scale), SV_EDTYPE, SV_EALIGN (q, k, v, cache or
  * out pointers or strides not multiples of 16 bytes), SV_EWORKSPACE, SV_EHIP.
  */
@@ -182,8 +182,8 @@ size_t specverify_tree_verify_workspace_size(int64_t B, int64_t V, int64_t max_n
  *   target_probs [T, V], rows t_stride apart: row i is the target's
  *                distribution after node i
  *   draft_probs  [T, V], rows d_stride apart: row i is the distribution that
- *                node i's children were drawn from (rows of leaves are not
- *                read); NULL for SV_DRAFT_FIXED
+ *                node i's children were drawn from (rows of leaves may hold
+ *                anything); NULL for SV_DRAFT_FIXED
  *   dtype        SV_F32 or SV_BF16, of both
  *   tokens       [T] int32 (a root's is not read), parents, node_start: the trees
  *   u            [T] double in [0, 1): node i's accept uniform (a root's is not read)
