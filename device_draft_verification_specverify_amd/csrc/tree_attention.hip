@@ -989,13 +989,15 @@ int specverify_tree_attention(
                              c_stride_token, c_stride_h, o_stride_t, o_stride_h};
   for (int64_t s : strides)
     if (s < 0) return SV_EINVAL;
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return SV_EINVAL;
+  if (!(scale > 0.0f) || !std::isfinite(scale * kLog2e)) return SV_EINVAL;
   if (dtype != SV_BF16 && dtype != SV_F16) return SV_EDTYPE;
   for (int64_t s : strides)
     if (s % 8 != 0) return SV_EALIGN;
   if (!aligned16(q) || !aligned16(k_tree) || !aligned16(v_tree) || !aligned16(k_cache) ||
       !aligned16(v_cache) || !aligned16(out))
     return SV_EALIGN;
+  const int64_t out_sizes[] = {T, Hq}, out_strides[] = {o_stride_t, o_stride_h};
+  if (!apart(2, out_sizes, out_strides, D)) return SV_EINVAL;
   int status = SV_OK;
   if (!workspace_ok(workspace, workspace_bytes,
                     specverify_tree_attention_workspace_size(B, T, Hq, Hkv, D, max_nodes),

@@ -289,6 +289,8 @@ int specverify_tree_commit(const void* k_tree, const void* v_tree, void* k_cache
     if (s * esz % 16 != 0) return SV_EALIGN;
   if (!aligned16(k_tree) || !aligned16(v_tree) || !aligned16(k_cache) || !aligned16(v_cache))
     return SV_EALIGN;
+  const int64_t c_sizes[] = {layers, num_pages, page_size, H};
+  if (!apart(4, c_sizes, strides + 3, D)) return SV_EINVAL;
   CommitArgs a{static_cast<const char*>(k_tree), static_cast<const char*>(v_tree),
                static_cast<char*>(k_cache), static_cast<char*>(v_cache),
                n_stride_l * esz, n_stride_t * esz, n_stride_h * esz, c_stride_l * esz,

@@ -36,6 +36,23 @@ inline bool workspace_ok(const void* ws, size_t have, size_t need, int* status) 
   return true;
 }
 
+// Whether the runs of `width` elements of an output lie apart: taken by rising
+// stride, each axis steps over all that the axes before it span.
+inline bool apart(int axes, const int64_t* sizes, const int64_t* strides, int64_t width) {
+  bool taken[4] = {};
+  __int128 span = width;
+  for (int round = 0; round < axes; ++round) {
+    int least = -1;
+    for (int i = 0; i < axes; ++i)
+      if (!taken[i] && (least < 0 || strides[i] < strides[least])) least = i;
+    taken[least] = true;
+    if (sizes[least] <= 1) continue;
+    if (strides[least] < span) return false;
+    span += __int128(strides[least]) * (sizes[least] - 1);
+  }
+  return true;
+}
+
 inline size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
 __device__ __forceinline__ void set_error(int32_t* err, int bits) {

@@ -89,8 +89,10 @@ def _want(t: torch.Tensor, dtype: torch.dtype, shape: tuple, dev: torch.device, 
 def _strided(t: torch.Tensor, dev: torch.device, ndim: int, name: str) -> tuple:
     """The strides of a tensor whose last axis is contiguous."""
     strides = t.stride()
-    if len(strides) != ndim or (strides[-1] != 1 and t.shape[-1] > 1 and t.numel()) or t.device != dev:
-        raise SpecVerifyError(f"{name}: want a {ndim}-d tensor on {dev} with a contiguous last axis")
+    if (len(strides) != ndim or (strides[-1] != 1 and t.shape[-1] > 1 and t.numel()) or
+            t.device != dev):
+        raise SpecVerifyError(f"{name}: want a {ndim}-d tensor on {dev} with a contiguous last "
+                              f"axis")
     return strides
 
 
@@ -120,6 +122,8 @@ def _table(t: torch.Tensor, B: int, dev: torch.device) -> tuple:
     rows, width = t.shape
     if t.dtype is not torch.int32 or rows != B:
         raise SpecVerifyError(f"block_table: want int32 [{B}, max_pages]")
+    if rows > 1 and stride < width:  # rows that overlap, as of an expanded tensor
+        raise SpecVerifyError(f"block_table: rows of {width} entries are {stride} apart")
     return width, max(width, stride)
 
 
@@ -138,6 +142,8 @@ def _scratch(ws: torch.Tensor | None, nbytes: int, dev: torch.device, name: str)
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)  # any contents will do
     if ws.device != dev:
         raise SpecVerifyError(f"ws is on {ws.device}, the tensors on {dev}")
+    if ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise SpecVerifyError("ws: want a contiguous uint8 tensor")
     return ws
 
 
@@ -214,8 +220,8 @@ def specverify_tree_attention(q: torch.Tensor, k_tree: torch.Tensor, v_tree: tor
     num_pages, page_size, Hkv, width = k_cache.shape
     B = prefix_len.numel()
     if k_tree.shape != (T, Hkv, D) or width != D:
-        raise SpecVerifyError("q [T, Hq, D], k_tree [T, Hkv, D] and k_cache [pages, page_size, Hkv, "
-                              "D] disagree")
+        raise SpecVerifyError("q [T, Hq, D], k_tree [T, Hkv, D] and k_cache [pages, page_size, "
+                              "Hkv, D] disagree")
     dt = _dtype(q, (torch.bfloat16, torch.float16), "q")
     if k_tree.dtype is not q.dtype or k_cache.dtype is not q.dtype:
         raise SpecVerifyError("q, the nodes' and the cache's types differ")
@@ -313,8 +319,8 @@ def specverify_tree_commit(k_tree: torch.Tensor, v_tree: torch.Tensor, k_cache: 
     L, T, H, D = k_tree.shape
     layers, num_pages, page_size, heads, width = k_cache.shape
     if layers != L or heads != H or width != D or k_cache.dtype is not k_tree.dtype:
-        raise SpecVerifyError("k_tree [layers, T, H, D] and k_cache [layers, pages, page_size, H, D] "
-                              "disagree")
+        raise SpecVerifyError("k_tree [layers, T, H, D] and k_cache [layers, pages, page_size, H, "
+                              "D] disagree")
     dt = _dtype(k_tree, tuple(_DTYPES), "k_tree")
     B = prefix_len.numel()
     max_path = path.shape[-1] if path.dim() else 0

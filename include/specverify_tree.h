@@ -141,8 +141,9 @@ size_t specverify_tree_attention_workspace_size(int64_t B, int64_t T, int64_t Hq
  *   ancestors   [T, ceil(max_nodes / 64)] uint64 as specverify_tree_plan
  *               writes it, or any other mask over the request's nodes (bits
  *               from n_b on are ignored); NULL: node i sees nodes 0 .. i
- *   scale       > 0 and finite
- *   out         [T, Hq, D], strides o_stride_t, o_stride_h; must not overlap an input
+ *   scale       > 0, scale / ln 2 finite
+ *   out         [T, Hq, D], strides o_stride_t, o_stride_h, one axis stepping over
+ *               all that the other spans; must not overlap an input
  *   lse         [T, Hq] float32 out or NULL: ln of the softmax's denominator
  * A row that sees nothing (empty prefix and mask) gives zeros and lse = -inf.
  * Values in masked places (nodes a row does not see, slots behind prefix_len)
@@ -155,8 +156,9 @@ size_t specverify_tree_attention_workspace_size(int64_t B, int64_t T, int64_t Hq
  * D no multiple of 8 or outside [8, 256], max_nodes outside [1, 128],
  * max_nodes * Hq / Hkv > 2^16, B * Hkv > 2^24, page_size no power of two,
  * max_pages < 1 or max_pages * page_size + max_nodes > 2^31 - 2^14, T * Hq >= 2^31,
- * num_pages < 1, negative stride, table_stride < max_pages, scale), SV_EDTYPE, SV_EALIGN (q, k, v, cache or
- * out pointers or strides not multiples of 16 bytes), SV_EWORKSPACE, SV_EHIP.
+ * num_pages < 1, negative stride, rows of out that overlap, table_stride <
+ * max_pages, scale), SV_EDTYPE, SV_EALIGN (q, k, v, cache or out pointers or
+ * strides not multiples of 16 bytes), SV_EWORKSPACE, SV_EHIP.
  */
 int specverify_tree_attention(
     const void* q, const void* k_tree, const void* v_tree, const void* k_cache,
@@ -233,7 +235,8 @@ int specverify_tree_verify(const void* target_probs, const void* draft_probs, in
  * slots[b, 0 ..], and the lengths advance.
  *   k_tree, v_tree   [layers, T, H, D], both with strides n_stride_l, n_stride_t, n_stride_h
  *   k_cache, v_cache [layers, num_pages, page_size, H, D], both with strides
- *                    c_stride_l, c_stride_page, c_stride_token, c_stride_h
+ *                    c_stride_l, c_stride_page, c_stride_token, c_stride_h; in
+ *                    some order each axis steps over all that those before span
  *   dtype            SV_F32, SV_BF16 or SV_F16
  *   path, accept_len as specverify_tree_verify writes them; slots as
  *                    specverify_tree_plan does (slots of different requests differ)
@@ -246,9 +249,9 @@ int specverify_tree_verify(const void* target_probs, const void* draft_probs, in
  * Status: SV_EINVAL (null pointer but device_error or, with T = 0, the nodes;
  * layers, B, H < 1, T < 0, D no multiple of 8 or outside [8, 256], max_nodes
  * outside [1, 128], max_path outside [1, max_nodes], num_pages < 1, page_size no
- * power of two, num_pages * page_size >= 2^40, layers * B >= 2^31, H >= 2^16, negative
- * stride), SV_EDTYPE, SV_EALIGN (pointers or strides of nodes or cache not
- * multiples of 16 bytes), SV_EHIP.
+ * power of two, num_pages * page_size >= 2^40, layers * B >= 2^31, H >= 2^16,
+ * negative stride, tokens of the cache that overlap), SV_EDTYPE, SV_EALIGN
+ * (pointers or strides of nodes or cache not multiples of 16 bytes), SV_EHIP.
  */
 int specverify_tree_commit(const void* k_tree, const void* v_tree, void* k_cache, void* v_cache,
                            int dtype, int64_t layers, int64_t B, int64_t T, int64_t H, int64_t D,

@@ -4,6 +4,7 @@ import os
 import re
 
 import pytest
+import torch
 
 import device_draft_verification_specverify_amd as sv
 from device_draft_verification_specverify_amd import tree
@@ -119,3 +120,42 @@ def test_workspace_sizes():
     assert lib.specverify_tree_verify_workspace_size(64, 128256, 9) > 0
     for bad in ((0, 10, 2), (1, 0, 2), (1, 10, 200), (1, 1 << 23, 2)):
         assert lib.specverify_tree_verify_workspace_size(*bad) == 0
+
+
+@pytest.mark.parametrize("over", [dict(ot=0), dict(oh=0), dict(oh=56), dict(ot=248), dict(ot=64),
+                                  dict(ot=64, oh=256), dict(ot=0, oh=0)])
+def test_attention_refuses_an_output_whose_rows_overlap(over):
+    assert call("specverify_tree_attention", ATT, **over) == EINVAL
+
+
+@pytest.mark.parametrize("scale", [3e38, 2.4e38])
+def test_attention_refuses_a_scale_that_overflows_in_base_two(scale):
+    assert call("specverify_tree_attention", ATT, scale=scale) == EINVAL
+
+
+@pytest.mark.parametrize("over", [dict(cl=0), dict(cp=0), dict(ct=0), dict(ch=0), dict(ch=56),
+                                  dict(cp=2040), dict(cl=18424), dict(ch=128)])
+def test_commit_refuses_a_cache_whose_tokens_overlap(over):
+    assert call("specverify_tree_commit", COM, **over) == EINVAL
+
+
+def test_binding_refuses_a_table_of_overlapping_rows():
+    dev = torch.device("cpu")
+    one = torch.zeros((1, 6), dtype=torch.int32)
+    assert tree._table(one, 1, dev) == (6, 6)
+    assert tree._table(torch.zeros((3, 9), dtype=torch.int32)[:, :6], 3, dev) == (6, 9)
+    assert tree._table(torch.zeros(20, dtype=torch.int32).as_strided((1, 6), (2, 1)), 1, dev)[1] == 6
+    for bad in (one.expand(3, 6), torch.zeros(20, dtype=torch.int32).as_strided((3, 6), (4, 1))):
+        with pytest.raises(sv.SpecVerifyError, match="block_table"):
+            tree._table(bad, 3, dev)
+
+
+def test_binding_refuses_a_workspace_of_fewer_bytes_than_it_shows():
+    dev = torch.device("cpu")
+    ok = torch.empty(1024, dtype=torch.uint8)
+    assert tree._scratch(ok, 512, dev, "size") is ok
+    for bad in (torch.empty(1, dtype=torch.uint8).expand(1 << 20), ok[::2], ok.to(torch.float32)):
+        with pytest.raises(sv.SpecVerifyError, match="ws"):
+            tree._scratch(bad, 512, dev, "size")
+    with pytest.raises(sv.SpecVerifyError, match="size"):
+        tree._scratch(None, 0, dev, "size")
