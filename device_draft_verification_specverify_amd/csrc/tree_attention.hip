@@ -138,6 +138,7 @@ __device__ __forceinline__ Req uniform_request(Args a, int64_t b) {
 // split (`whole`): one place each, and nothing to join (32 requests of up to 600
 // tokens: 25 us so, 30 us split; 256 requests, with 8 items a worker, 170 us so,
 // 147 us split).
+constexpr int kWorkers = 256;  // one to a CU
 constexpr int kItemPlaces = 3;
 constexpr int kWholeTiles = 6;
 __device__ __forceinline__ int item_places(int whole, int tiles) {
@@ -156,11 +157,6 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
 __device__ __forceinline__ int64_t share_start(int64_t total, int workers, int64_t w) {
   const int64_t q = total / workers, rem = total % workers;
   return w * q + (w < rem ? w : rem);
-}
-__device__ __forceinline__ int64_t worker_of(int64_t total, int workers, int64_t tile) {
-  const int64_t q = total / workers, rem = total % workers;
-  const int64_t big = rem * (q + 1);
-  return tile < big ? tile / (q + 1) : rem + (tile - big) / q;
 }
 
 // Where the 16-byte piece c of row r of a tile lies (in pieces of its row): 16
@@ -846,56 +842,103 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
 }
 
 // Joins the shares of items that several workers had. The worker that comes
-// second in an item stands for it; blockIdx.y counts groups of its rows. DP / 4
-// lanes take a row.
+// second in an item stands for it; every workgroup counts those items' rows for
+// itself, a unit is as many rows as it takes at once (DP / 4 lanes each), and
+// units go round robin. Bound by the trips to memory one after another, so AHEAD
+// shares are asked for at once: 16 items of 136 rows in 17 shares each 8.2 us, 128
+// items of 256 rows (35 MB of shares) 10.8 us. (A workgroup for each possible unit,
+// most of them without work, and a share at a time: 16.2 and 15.7 us.)
+constexpr int kJoiners = 2048;
 template <int DT, int DP>
-__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int workers) {
+__global__ __launch_bounds__(kWorkers) void join_kernel(AttnArgs a) {
   using elem = typename Elem<DT>::type;
-  constexpr int LANES = DP / 4, ROWS = 256 / LANES;
-  const int64_t second = blockIdx.x;
-  const Split sp = a.split[second];
-  if (sp.tiles == 0) return;
-  const int r = sp.row0 + int(blockIdx.y) * ROWS + int(threadIdx.x) / LANES;
-  if (r >= sp.rows) return;
-  const int64_t total = a.split[workers].start;
-  const int64_t w0 = worker_of(total, workers, sp.start);
-  if (w0 + 1 != second) return;
-  const int64_t w1 = worker_of(total, workers, sp.start + sp.tiles - 1);
-  const int64_t step = int64_t(a.tile_rows) * (DP + 4);
-  const float* p = a.part + int64_t(r - sp.row0) * (DP + 4);
-  const int d0 = int(threadIdx.x) % LANES * 4;
-  // w0's share is its last segment, the others' their first
-  float m = -INFINITY, l = 0.0f;
-  f32x4 x = {0, 0, 0, 0};
-  for (int64_t w = w0; w <= w1; ++w) {
-    const float* o = p + (w * 2 + (w == w0 ? 1 : 0)) * step;
-    const f32x4 y = *reinterpret_cast<const f32x4*>(o + d0);
-    const float mw = o[DP], lw = o[DP + 1];
-    const float to = fmaxf(m, mw), ref = to == -INFINITY ? 0.0f : to;
-    const float f = __builtin_amdgcn_exp2f(m - ref), g = __builtin_amdgcn_exp2f(mw - ref);
-    l = l * f + lw * g;
-    x = x * f + y * g;
-    m = to;
+  constexpr int LANES = DP / 4, ROWS = kWorkers / LANES, AHEAD = 4;
+  __shared__ Split item;
+  __shared__ int item_second, item_unit, wave_units[kWorkers / kWave];
+  const int tid = int(threadIdx.x), lane = tid % kWave;
+  const Split own = a.split[tid];
+  const int64_t total = a.split[kWorkers].start;
+  const bool stands = own.tiles > 0 && share_start(total, kWorkers, tid - 1) <= own.start;
+  const int units = stands ? (min(own.rows - own.row0, a.tile_rows) + ROWS - 1) / ROWS : 0;
+  int upto = units;
+  for (int d = 1; d < kWave; d *= 2) {
+    const int y = __shfl_up(upto, d);
+    if (lane >= d) upto += y;
   }
-  const int node = r / a.G;
-  const int hq = sp.h * a.G + r - node * a.G;
-  const bool some = l > 0.0f || l != l;
-  const float inv = some ? 1.0f / l : 0.0f;
-  if (d0 < a.D) {
-    typedef elem e4 __attribute__((ext_vector_type(4)));
-    e4 y;
-    for (int k = 0; k < 4; ++k) y[k] = elem(x[k] * inv);
-    *reinterpret_cast<e4*>(a.out + (sp.first + node) * a.o_t + hq * a.o_h + d0 * 2) = y;
+  if (lane == kWave - 1) wave_units[tid / kWave] = upto;
+  __syncthreads();
+  int all = 0;
+  for (int k = 0; k < kWorkers / kWave; ++k) {
+    if (k < tid / kWave) upto += wave_units[k];
+    all += wave_units[k];
   }
-  if (a.lse && d0 == 0)
-    a.lse[(sp.first + node) * a.Hq + hq] =
-        some ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+  for (int u = int(blockIdx.x); u < all; u += int(gridDim.x)) {
+    if (u >= upto - units && u < upto) {
+      item = own;
+      item_second = tid;
+      item_unit = u - (upto - units);
+    }
+    __syncthreads();
+    const Split sp = item;
+    const int second = item_second;
+    const int in_tile = item_unit * ROWS + tid / LANES, r = sp.row0 + in_tile;
+    __syncthreads();
+    if (in_tile >= a.tile_rows || r >= sp.rows) continue;
+    const int64_t step = int64_t(a.tile_rows) * (DP + 4);
+    const float* p = a.part + int64_t(in_tile) * (DP + 4);
+    const int d0 = tid % LANES * 4;
+    // the first one's share is its last segment, the others' their first
+    float m = -INFINITY, l = 0.0f;
+    f32x4 x = {0, 0, 0, 0};
+    const auto has = [&](int w) {
+      return w < kWorkers && share_start(total, kWorkers, w) < sp.start + sp.tiles;
+    };
+    const auto add = [&](f32x4 y, float mw, float lw) {
+      const float to = fmaxf(m, mw), ref = to == -INFINITY ? 0.0f : to;
+      const float f = __builtin_amdgcn_exp2f(m - ref), g = __builtin_amdgcn_exp2f(mw - ref);
+      l = l * f + lw * g;
+      x = x * f + y * g;
+      m = to;
+    };
+    const auto share_of = [&](int w) { return p + (w * 2 + (w < second ? 1 : 0)) * step; };
+    int w = second - 1;
+    for (; has(w + AHEAD - 1); w += AHEAD) {
+      f32x4 y[AHEAD];
+      float mw[AHEAD], lw[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const float* o = share_of(w + i);
+        y[i] = *reinterpret_cast<const f32x4*>(o + d0);
+        mw[i] = o[DP];
+        lw[i] = o[DP + 1];
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) add(y[i], mw[i], lw[i]);
+    }
+    for (; has(w); ++w) {
+      const float* o = share_of(w);
+      add(*reinterpret_cast<const f32x4*>(o + d0), o[DP], o[DP + 1]);
+    }
+    const int node = r / a.G;
+    const int hq = sp.h * a.G + r - node * a.G;
+    const bool some = l > 0.0f || l != l;
+    const float inv = some ? 1.0f / l : 0.0f;
+    if (d0 < a.D) {
+      typedef elem e4 __attribute__((ext_vector_type(4)));
+      e4 y;
+      for (int k = 0; k < 4; ++k) y[k] = elem(x[k] * inv);
+      *reinterpret_cast<e4*>(a.out + (sp.first + node) * a.o_t + hq * a.o_h + d0 * 2) = y;
+    }
+    if (a.lse && d0 == 0)
+      a.lse[(sp.first + node) * a.Hq + hq] =
+          some ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+  }
 }
 
 // Which kernel: rows of the largest tree in wavefronts of 32 rows, and the rest
 // of a workgroup along the keys.
 struct Variant {
-  int rw, kw, kb, width, workers;
+  int rw, kw, kb, width;
 };
 Variant variant_of(int64_t rows, int64_t D) {
   Variant v;
@@ -908,13 +951,12 @@ Variant variant_of(int64_t rows, int64_t D) {
     v.kw = v.rw == 1 ? 4 : 8 / v.rw;
     v.kb = v.rw == 8 ? 64 : 32;
   }
-  v.workers = 256;
   return v;
 }
 
 template <int DT, int DP, int RW, int KW, int KB, int S>
 void launch_one(const Variant& v, const AttnArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((attention_kernel<DT, DP, RW, KW, KB, S>), dim3(unsigned(v.workers)),
+  hipLaunchKernelGGL((attention_kernel<DT, DP, RW, KW, KB, S>), dim3(unsigned(kWorkers)),
                      dim3(64 * RW * KW), 0, st, a);
 }
 
@@ -937,8 +979,7 @@ template <int DT, int DP>
 void launch_both(const Variant& v, const AttnArgs& a, hipStream_t st) {
   launch<DT, DP>(v, a, st);
   if (a.whole) return;
-  const dim3 grid{unsigned(v.workers), unsigned(32 * v.rw * DP / 1024)};
-  hipLaunchKernelGGL((join_kernel<DT, DP>), grid, dim3(256), 0, st, a, v.workers);
+  hipLaunchKernelGGL((join_kernel<DT, DP>), dim3(kJoiners), dim3(kWorkers), 0, st, a);
 }
 
 template <int DT>
@@ -964,8 +1005,8 @@ size_t specverify_tree_attention_workspace_size(int64_t B, int64_t T, int64_t Hq
                                                 int64_t D, int64_t max_nodes) {
   if (!sizes_ok(B, T, Hq, Hkv, D, max_nodes)) return 0;
   const Variant v = variant_of(max_nodes * (Hq / Hkv), D);
-  return align256(size_t(v.workers + 1) * sizeof(Split)) +
-         align256(size_t(v.workers) * 2 * (32 * v.rw) * (v.width + 4) * sizeof(float));
+  return align256(size_t(kWorkers + 1) * sizeof(Split)) +
+         align256(size_t(kWorkers) * 2 * (32 * v.rw) * (v.width + 4) * sizeof(float));
 }
 
 int specverify_tree_attention(
@@ -1042,13 +1083,13 @@ int specverify_tree_attention(
   a.scale_log2 = scale * kLog2e;
   a.split = static_cast<Split*>(workspace);
   a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                    align256(size_t(v.workers + 1) * sizeof(Split)));
+                                    align256(size_t(kWorkers + 1) * sizeof(Split)));
   a.tile_keys = v.kw * v.kb;
   a.tile_rows = 32 * v.rw;
   a.width = v.width;
   const int64_t items = B * Hkv * ((max_nodes * (Hq / Hkv) + a.tile_rows - 1) / a.tile_rows);
   a.whole = max_pages * page_size + max_nodes <= kWholeTiles * int64_t(a.tile_keys) &&
-            items <= v.workers;
+            items <= kWorkers;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (dtype == SV_BF16) launch_width<SV_BF16>(v, a, st);
   else launch_width<SV_F16>(v, a, st);
