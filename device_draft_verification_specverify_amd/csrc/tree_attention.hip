@@ -936,20 +936,31 @@ __global__ __launch_bounds__(kWorkers) void join_kernel(AttnArgs a) {
 }
 
 // Which kernel: rows of the largest tree in wavefronts of 32 rows, and the rest
-// of a workgroup along the keys.
+// of a workgroup along the keys. Fewer rows leave some wavefronts without
+// products, more than a workgroup has would read the keys once more.
+//   up to 64 rows: 64 single tokens, heads of 64, 224 us, 253 us with the kernel of
+//     128 rows (heads of 128 alike, 414 and 408 us; a kernel of 32 rows for them
+//     took 416 us)
+//   up to 128: 32 trees of 32 nodes 157 us, 165 us with the kernel of 256 rows; 178
+//     us with tiles of 64 keys (32 a wavefront), 193 us without wavefronts along
+//     the keys; heads of 64: 93 and 113 us
+//   more: 16 trees of 64 nodes 222 us, 243 us in two tiles of 128 rows
+// Heads wider than 128 (registers for 4 wavefronts): 64 rows 110 us, 125 us with the
+// kernel of 128 rows; 16 rows 187 and 200 us, 269 us with one of 32.
 struct Variant {
   int rw, kw, kb, width;
 };
 Variant variant_of(int64_t rows, int64_t D) {
   Variant v;
   v.width = D <= 64 ? 64 : D <= 128 ? 128 : 256;
-  v.rw = rows <= 32 ? 1 : rows <= 64 ? 2 : rows <= 128 || v.width == 256 ? 4 : 8;
   if (v.width == 256) {
-    v.kw = v.rw == 1 ? 2 : v.rw == 2 ? 2 : 1;
+    v.rw = rows <= 64 ? 2 : 4;
+    v.kw = 4 / v.rw;
     v.kb = 32;
   } else {
-    v.kw = v.rw == 1 ? 4 : 8 / v.rw;
-    v.kb = v.rw == 8 ? 64 : 32;
+    v.rw = rows <= 64 ? 2 : rows <= 128 ? 4 : 8;
+    v.kw = 8 / v.rw;
+    v.kb = v.rw == 2 ? 32 : 64;
   }
   return v;
 }
@@ -963,14 +974,12 @@ void launch_one(const Variant& v, const AttnArgs& a, hipStream_t st) {
 template <int DT, int DP>
 void launch(const Variant& v, const AttnArgs& a, hipStream_t st) {
   if constexpr (DP == 256) {
-    if (v.rw == 1) launch_one<DT, DP, 1, 2, 32, 2>(v, a, st);
-    else if (v.rw == 2) launch_one<DT, DP, 2, 2, 32, 2>(v, a, st);
+    if (v.rw == 2) launch_one<DT, DP, 2, 2, 32, 2>(v, a, st);
     else launch_one<DT, DP, 4, 1, 32, 4>(v, a, st);
   } else {
     constexpr int X = 128 / DP;  // stages of half the size, twice as many
-    if (v.rw == 1) launch_one<DT, DP, 1, 4, 32, 2 * X>(v, a, st);
-    else if (v.rw == 2) launch_one<DT, DP, 2, 4, 32, 2 * X>(v, a, st);
-    else if (v.rw == 4) launch_one<DT, DP, 4, 2, 32, 4>(v, a, st);
+    if (v.rw == 2) launch_one<DT, DP, 2, 4, 32, 2 * X>(v, a, st);
+    else if (v.rw == 4) launch_one<DT, DP, 4, 2, 64, 2 * X>(v, a, st);
     else launch_one<DT, DP, 8, 1, 64, 4>(v, a, st);
   }
 }
