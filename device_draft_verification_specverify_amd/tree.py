@@ -177,7 +177,7 @@ def specverify_tree_plan(parents: torch.Tensor, node_start: torch.Tensor, prefix
     width, stride = _table(block_table, B, dev)
     err = _optional(device_error, i32, (1,), dev, "device_error")
     empty = torch.empty
-    ancestors = empty((T, (max_nodes + 63) // 64), dtype=torch.int64, device=dev)
+    ancestors = empty((T, max((max_nodes + 63) // 64, 0)), dtype=torch.int64, device=dev)
     depth = empty(T, dtype=i32, device=dev)
     position = empty(T, dtype=i32, device=dev)
     slots = empty((B, max(max_path, 0)), dtype=torch.int64, device=dev)

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import device_draft_verification_specverify_amd as sv
 import test_gpu_tree_attention as att
 import test_gpu_tree_cache as cache
 import test_gpu_tree_verify as ver
@@ -104,3 +105,17 @@ def test_commit_behind_32_bits():
     for k, x in near.items():
         assert np.array_equal(cache.bits(c[k]), x), k
     assert cache.check_commit(c) == 0
+
+
+@pytest.mark.parametrize("over", [dict(max_nodes=-100), dict(max_nodes=0), dict(max_path=-1),
+                                  dict(max_path=6), dict(page_size=24), dict(num_pages=0)])
+def test_plan_refuses_sizes_before_any_work(over):
+    i32 = dict(dtype=torch.int32, device=DEV)
+    table = torch.full((1, 4), -1, **i32)
+    sizes = dict(page_size=16, num_pages=8, max_nodes=5, max_path=5) | over
+    with pytest.raises(sv.SpecVerifyError, match="status -1"):
+        ver.tree.specverify_tree_plan(
+            torch.tensor([-1, 0], **i32), torch.tensor([0, 2], **i32), torch.zeros(1, **i32),
+            torch.zeros(1, **i32), table, torch.arange(8, **i32), torch.zeros(1, **i32), **sizes)
+    torch.cuda.synchronize()
+    assert torch.all(table == -1)
