@@ -13,6 +13,14 @@
 // j < 4 and 8 + 4 h + j - 4 for the rest, which is how the accumulator holds
 // them. V^T fragments come from the row-major tile by the transposing LDS read
 // (4 keys x 16 columns per 16 lanes).
+//
+// What bounds it, heads of 128 in bf16: for few rows memory, with a ring of tiles
+// in LDS kept full over the ends of items (64 single tokens over 1000 to 16000 keys
+// 414 us, 5.4 TB/s; 64 chains of 9 over 301 to 8011 keys 231 us, 4.8 TB/s); for
+// many rows each wavefront's own chain of LDS reads, products and exponentials
+// (16 trees of 64 nodes, 256 rows an item: 198 us, 3.0 TB/s and 0.56 PFLOP/s; per
+// 64 keys fetch 0.6 us, K Q 0.5, softmax 0.4, P V 0.64, barrier 0.6); for a few
+// hundred keys latency (one token over 500: 18 us).
 
 #include "tree_common.h"
 
@@ -136,8 +144,8 @@ __device__ __forceinline__ Req uniform_request(Args a, int64_t b) {
 // loaded, wavefronts joined, results written).
 // Where no request can have many tiles and every item has a worker, items are not
 // split (`whole`): one place each, and nothing to join (32 requests of up to 600
-// tokens: 25 us so, 30 us split; 256 requests, with 8 items a worker, 170 us so,
-// 147 us split).
+// tokens: 24 us so, 30 us split; one token over 500 keys 20 and 22 us; 256
+// requests, with 8 items a worker, 170 us so, 147 us split).
 constexpr int kWorkers = 256;  // one to a CU
 constexpr int kItemPlaces = 3;
 constexpr int kWholeTiles = 6;
