@@ -184,6 +184,7 @@ __device__ __forceinline__ double scan_wave(double x) {
 
 struct Shared {
   double front[kMaxChunks];   // mass of the chunks up to and with each
+  uint64_t some[kMaxChunks / kWave];  // a bit for each chunk that has mass itself
   double wave[4][kWaves];
   double px[SV_MAX_TREE_NODES], qx[SV_MAX_TREE_NODES], u[SV_MAX_TREE_NODES];
   int32_t tok[SV_MAX_TREE_NODES], up[SV_MAX_TREE_NODES];
@@ -241,8 +242,8 @@ __device__ __forceinline__ uint64_t chunk_masses(const Weights& w, Get get, Shar
   return t != t ? kWrong : (uint64_t)__double_as_longlong(t);
 }
 
-// Mass of the weights: running sums of the chunks to sm.front, the whole
-// returned to every thread (NaN for a wrong row).
+// Mass of the weights: running sums of the chunks to sm.front, which of them have
+// any to sm.some, the whole returned to every thread (NaN for a wrong row).
 //
 // The workgroups of a request run the same walk side by side; each takes its
 // share of a pass's chunks and publishes their sums, which are value and flag in
@@ -312,7 +313,10 @@ __device__ __forceinline__ double mass_of(const VerifyArgs& a, const Weights& w,
   if (tid < kWave) {
     double before = 0.0;
     for (int c = lane; c - lane < chunks; c += kWave) {
-      const double s = before + scan_wave(c < chunks ? sm.front[c] : 0.0);
+      const double own = c < chunks ? sm.front[c] : 0.0;
+      const uint64_t some = __ballot(own > 0.0);
+      if (lane == 0) sm.some[c / kWave] = some;
+      const double s = before + scan_wave(own);
       if (c < chunks) sm.front[c] = s;
       before = __shfl(s, kWave - 1);
     }
@@ -324,6 +328,10 @@ __device__ __forceinline__ double mass_of(const VerifyArgs& a, const Weights& w,
 // The least id whose running sum exceeds x, after mass_of of the same weights;
 // the last one with a weight when rounding leaves none. -1 from a workgroup that
 // does not own the id's chunk.
+//
+// The scan adds the chunks before two neighbours in different orders, so their
+// running sums may differ in the last bit with no mass between them: a chunk
+// without mass is never taken, whatever its running sum.
 template <int DT, bool VEC>
 __device__ __forceinline__ int32_t pick(const VerifyArgs& a, const Weights& w, double x, int share, Shared& sm,
                         bool* mine) {
@@ -331,11 +339,13 @@ __device__ __forceinline__ int32_t pick(const VerifyArgs& a, const Weights& w, d
   const int chunks = a.chunks;
   const double whole = sm.front[chunks - 1];
   const bool over = !(x < whole);
-  if (tid == 0) sm.found_chunk = chunks - 1;
+  int word = (chunks - 1) / kWave;
+  while (word > 0 && !sm.some[word]) --word;
+  if (tid == 0) sm.found_chunk = word * kWave + kWave - 1 - __builtin_clzll(sm.some[word] | 1);
   __syncthreads();
-  // the first chunk whose running sum passes x, or reaches the whole
-  for (int c = tid; c < chunks; c += kBlock)
-    if (over ? sm.front[c] >= whole : sm.front[c] > x) {
+  // the first chunk with mass whose running sum passes x, or the last with mass
+  for (int c = tid; c < chunks && !over; c += kBlock)
+    if ((sm.some[c / kWave] >> (c % kWave) & 1) && sm.front[c] > x) {
       atomicMin(&sm.found_chunk, c);
       break;
     }
