@@ -901,11 +901,17 @@ __global__ __launch_bounds__(kWorkers) void join_kernel(AttnArgs a) {
     const auto has = [&](int w) {
       return w < kWorkers && share_start(total, kWorkers, w) < sp.start + sp.tiles;
     };
+    // an infinite sum stays so however little its share weighs, as within a share
+    const auto weighed = [](f32x4 v, float f) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = fabsf(v[k]) == INFINITY ? v[k] : v[k] * f;
+      return v;
+    };
     const auto add = [&](f32x4 y, float mw, float lw) {
       const float to = fmaxf(m, mw), ref = to == -INFINITY ? 0.0f : to;
       const float f = __builtin_amdgcn_exp2f(m - ref), g = __builtin_amdgcn_exp2f(mw - ref);
       l = l * f + lw * g;
-      x = x * f + y * g;
+      x = weighed(x, f) + weighed(y, g);
       m = to;
     };
     const auto share_of = [&](int w) { return p + (w * 2 + (w < second ? 1 : 0)) * step; };

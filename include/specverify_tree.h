@@ -147,7 +147,10 @@ size_t specverify_tree_attention_workspace_size(int64_t B, int64_t T, int64_t Hq
  *   lse         [T, Hq] float32 out or NULL: ln of the softmax's denominator
  * A row that sees nothing (empty prefix and mask) gives zeros and lse = -inf.
  * Values in masked places (nodes a row does not see, slots behind prefix_len)
- * do not reach it, also when they are infinite or NaN. A page outside
+ * do not reach it, also when they are infinite or NaN. An infinite or NaN value
+ * of a node that a row sees becomes that row's in its column, whatever its
+ * weight; one in the cache makes the column of every row of its request and head
+ * infinite or NaN. A page outside
  * [0, num_pages) counts as zero keys and values (SV_ERR_PAGE); a prefix_len
  * outside [0, max_pages * page_size] is clamped to it (SV_ERR_LENGTH); the rows
  * of a request with a wrong node_start are left as they were (SV_ERR_TREE).
