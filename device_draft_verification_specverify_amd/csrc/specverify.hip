@@ -46,6 +46,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "device_checks.h"
 #include "specverify.h"
 
 namespace {
@@ -173,22 +174,6 @@ __device__ __forceinline__ double accept_log_u(uint64_t seed, const int64_t* pos
                                   uint32_t(seed >> 32));
   return log_uniform_d(unit_uniform_d(w.w[0]));
 }
-
-// ---------------------------------------------------------------------------
-// Device-side index checks (a build with -DSV_DEVICE_CHECKS): a work unit checks
-// the indices it derived against the sizes it was launched with before it
-// touches memory; a failed check is counted in sv_check_count (read by
-// specverify_check_count) and the unit is skipped. In the product build sv_ok
-// is true and the checks fold away.
-#ifdef SV_DEVICE_CHECKS
-__device__ unsigned int sv_check_count;
-__device__ __forceinline__ bool sv_ok(bool ok) {
-  if (!ok) atomicAdd(&sv_check_count, 1u);
-  return ok;
-}
-#else
-__device__ __forceinline__ bool sv_ok(bool) { return true; }
-#endif
 
 // ---------------------------------------------------------------------------
 // Logit access. A "vector" is 8 consecutive logits starting at a multiple of 8.
@@ -3188,13 +3173,11 @@ int specverify_branch_prune(const float* logq, int64_t B, int64_t K, int64_t gam
 int specverify_check_count(uint32_t* count, int reset) {
 #ifdef SV_DEVICE_CHECKS
   if (!count) return SV_EINVAL;
-  if (hipMemcpyFromSymbol(count, HIP_SYMBOL(sv_check_count), sizeof(uint32_t)) != hipSuccess)
+  uint32_t sum = 0;
+  if (!sv_add_checks(&sum, reset) || !sv_add_tree_cache_checks(&sum, reset) ||
+      !sv_add_tree_verify_checks(&sum, reset) || !sv_add_tree_attention_checks(&sum, reset))
     return SV_EHIP;
-  if (reset) {
-    const uint32_t zero = 0;
-    if (hipMemcpyToSymbol(HIP_SYMBOL(sv_check_count), &zero, sizeof zero) != hipSuccess)
-      return SV_EHIP;
-  }
+  *count = sum;
   return SV_OK;
 #else
   (void)count;

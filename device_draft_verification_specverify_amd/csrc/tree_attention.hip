@@ -299,6 +299,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   }
   const int64_t at = uniform(share_start(total, workers, w));
   const int64_t end = uniform(share_start(total, workers, w + 1));
+  if (!sv_ok(workers == kWorkers && w < workers && at <= end && end <= total)) return;
   if (w == 0 && tid == 0) a.split[workers].start = total;
   if (at >= end) return;
   // the request that holds tile `at`: more than NT of them are gone through again
@@ -366,7 +367,8 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   // this lane's page id in the batch of tiles from t on (the prefix's last at most)
   auto id_place = [&](const int32_t* table, int t, int len) __attribute__((always_inline)) {
     const int key = (t + lane / UNITS) * KT + lane % UNITS * (NT / CPR) + wv * WROWS;
-    return table + ((key < len ? key : len - 1) >> page_shift);
+    const int at = (key < len ? key : len - 1) >> page_shift;
+    return table + (sv_ok(at >= 0 && at < a.max_keys >> page_shift) ? at : 0);
   };
   auto take_ids = [&](int box) __attribute__((always_inline)) {
     ids = id_box[wv][box][lane];
@@ -402,6 +404,11 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
       sg.rt = item - sg.h * rq.row_tiles;
       at += p1 - p0;
     } while (sg.t0 == sg.t1);
+    if (!sv_ok(b < s->B && sg.h >= 0 && sg.h < s->Hkv && sg.rt < rq.row_tiles && sg.t0 < sg.t1 &&
+               sg.t1 <= rq.tiles && rq.first + rq.n <= s->T)) {
+      more = false;
+      return;
+    }
     sg.first = rq.first;
     sg.n = rq.n;
     sg.len = rq.len;
@@ -443,6 +450,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
       f_tiles = f_t1 - f_t;
     }
     const int t = f_t++;
+    if (!sv_ok(to_stage < S && t * KT < f_keys && f_seg <= prepared)) return false;
     const uint32_t stage = tile_at + uint32_t(to_stage) * STAGE + wv * 1024;
     if (t - f_batch == BATCH) {
       f_batch = t;
@@ -528,6 +536,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
     const int r = row0 + col < n * s->G ? row0 + col : 0;
     const int node = r / s->G;
     const int64_t i = uniform(sg.first) + node;
+    if (!sv_ok(node < n && i < s->T)) return;
     const char* qp = s->q + i * s->q_t + (h * s->G + r - node * s->G) * s->q_h;
 #pragma unroll
     for (int k = 0; k < DP / 16; ++k) {
@@ -803,7 +812,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
       }
 
       rows_here();
-      if (row_ok) {
+      if (row_ok && sv_ok(first + node < s->T && hq < s->Hq)) {
         if (whole) {
           const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
           char* op = s->out + (first + node) * s->o_t + hq * s->o_h + 8 * half;
@@ -935,6 +944,7 @@ __global__ __launch_bounds__(kWorkers) void join_kernel(AttnArgs a) {
     }
     const int node = r / a.G;
     const int hq = sp.h * a.G + r - node * a.G;
+    if (!sv_ok(sp.first + node < a.T && hq < a.Hq && w <= kWorkers)) continue;
     const bool some = l > 0.0f || l != l;
     const float inv = some ? 1.0f / l : 0.0f;
     if (d0 < a.D) {
@@ -1021,6 +1031,10 @@ bool sizes_ok(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t 
 }
 
 }  // namespace
+
+#ifdef SV_DEVICE_CHECKS
+bool sv_add_tree_attention_checks(uint32_t* count, int reset) { return sv_add_checks(count, reset); }
+#endif
 
 extern "C" {
 

@@ -61,6 +61,7 @@ __device__ __forceinline__ Need need_of(const PlanArgs& a, int64_t b) {
 __global__ __launch_bounds__(kPlanBlock) void plan_kernel(PlanArgs a) {
   const int64_t b = blockIdx.x;
   const int tid = int(threadIdx.x);
+  if (!sv_ok(b < a.B)) return;
   const Nodes nd = nodes_of(a.node_start, b, a.T, a.max_nodes);
   const Need me = need_of(a, b);
   const int64_t head = *a.head_in;
@@ -95,6 +96,7 @@ __global__ __launch_bounds__(kPlanBlock) void plan_kernel(PlanArgs a) {
 
   int32_t* row = a.table + b * a.table_stride;
   for (int32_t j = tid; j < more; j += kPlanBlock) {
+    if (!sv_ok(me.owned + j < a.max_pages && head + before + j < a.num_free)) continue;
     const int32_t id = a.free_pages[head + before + j];
     const bool good = id >= 0 && id < a.num_pages;
     row[me.owned + j] = good ? id : -1;
@@ -110,7 +112,7 @@ __global__ __launch_bounds__(kPlanBlock) void plan_kernel(PlanArgs a) {
   bool wrong = false;
   uint64_t m0 = 0, m1 = 0;
   if (mine) {
-    up = a.parents[nd.first + tid];
+    up = sv_ok(nd.first + tid < a.T) ? a.parents[nd.first + tid] : -1;
     wrong = tid == 0 ? up != -1 : (up < 0 || up >= tid);
     if (wrong) up = -1;
     (tid < 64 ? m0 : m1) = uint64_t(1) << (tid & 63);
@@ -133,7 +135,7 @@ __global__ __launch_bounds__(kPlanBlock) void plan_kernel(PlanArgs a) {
   const int32_t deep = __popcll(m0) + __popcll(m1) - 1;
   bad_tree = __syncthreads_or(mine && deep >= a.max_path) || bad_tree;
   if (bad_tree) bits |= SV_ERR_TREE;
-  if (mine) {
+  if (mine && sv_ok(nd.first + tid < a.T)) {
     const int64_t i = nd.first + tid;
     a.ancestors[i * a.words] = bad_tree ? 0 : m0;
     if (a.words > 1) a.ancestors[i * a.words + 1] = bad_tree ? 0 : m1;
@@ -146,6 +148,8 @@ __global__ __launch_bounds__(kPlanBlock) void plan_kernel(PlanArgs a) {
     if (i < me.tokens && me.ok && fits && !bad_tree) {
       const int64_t at = int64_t(me.len) + i;
       const int64_t pg = at >> a.page_shift;
+      if (!sv_ok(pg < a.max_pages && (pg < me.owned || head + before + pg - me.owned < a.num_free)))
+        continue;
       const int32_t id = pg < me.owned ? row[pg] : a.free_pages[head + before + (pg - me.owned)];
       if (id >= 0 && id < a.num_pages)
         slot = (int64_t(id) << a.page_shift) | (at & ((int64_t(1) << a.page_shift) - 1));
@@ -175,6 +179,7 @@ struct CommitArgs {
   const int32_t* len_in;
   int32_t* len_out;
   int32_t* err;
+  int64_t layers;
 };
 
 // One workgroup per (request, layer): its threads take the 16-byte pieces of a
@@ -184,6 +189,7 @@ struct CommitArgs {
 __global__ __launch_bounds__(kCommitBlock) void commit_kernel(CommitArgs a) {
   const int64_t b = int64_t(blockIdx.x) % a.B, layer = int64_t(blockIdx.x) / a.B;
   const int tid = int(threadIdx.x);
+  if (!sv_ok(layer < a.layers)) return;
   __shared__ int64_t src[SV_MAX_TREE_NODES], dst[SV_MAX_TREE_NODES];
   const Nodes nd = nodes_of(a.node_start, b, a.T, a.max_nodes);
   const int32_t taken = a.accept_len[b];
@@ -210,6 +216,7 @@ __global__ __launch_bounds__(kCommitBlock) void commit_kernel(CommitArgs a) {
     const bool val = e >= per;
     const int r = val ? e - per : e;
     const int h = r / a.chunks, c = r - h * a.chunks;
+    if (!sv_ok(h < a.H && c >= 0 && nd.first + nd.n <= a.T)) continue;
     const char* from = (val ? a.v_tree : a.k_tree) + h * a.n_h + c * 16;
     char* to = (val ? a.v_cache : a.k_cache) + h * a.c_h + c * 16;
     for (int i = 0; i <= taken; i += 4) {
@@ -227,6 +234,10 @@ __global__ __launch_bounds__(kCommitBlock) void commit_kernel(CommitArgs a) {
 bool under31(int64_t x) { return x < (int64_t(1) << 31); }
 
 }  // namespace
+
+#ifdef SV_DEVICE_CHECKS
+bool sv_add_tree_cache_checks(uint32_t* count, int reset) { return sv_add_checks(count, reset); }
+#endif
 
 extern "C" {
 
@@ -297,7 +308,7 @@ int specverify_tree_commit(const void* k_tree, const void* v_tree, void* k_cache
                c_stride_page * esz, c_stride_token * esz, c_stride_h * esz,
                B, T, num_pages * page_size, int(H), int(D * esz / 16), int(max_nodes),
                int(max_path), log2_of(page_size), node_start, path, accept_len, slots,
-               prefix_len_in, prefix_len_out, device_error};
+               prefix_len_in, prefix_len_out, device_error, layers};
   hipLaunchKernelGGL(commit_kernel, dim3(unsigned(layers * B)), dim3(kCommitBlock), 0,
                      reinterpret_cast<hipStream_t>(stream), a);
   return launch_status();

@@ -8,6 +8,7 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "device_checks.h"
 #include "specverify_tree.h"
 
 namespace svtree {

@@ -56,6 +56,7 @@ struct VerifyArgs {
   int32_t* emitted;
   int32_t* out_token;
   int32_t* err;
+  int64_t B;
 };
 
 template <int DT>
@@ -262,6 +263,7 @@ __device__ __forceinline__ double mass_of(const VerifyArgs& a, const Weights& w,
   const int chunks = a.chunks;
   int c0 = int(int64_t(chunks) * share / a.spread);
   int c1 = int(int64_t(chunks) * (share + 1) / a.spread);
+  if (!sv_ok(0 <= c0 && c0 < c1 && c1 <= chunks)) return NAN;
   for (bool own = true;; own = false) {
     for (int c = c0; c < c1; c += kAtOnce<VEC>) {
       if (!own) {  // only where one is missing
@@ -353,7 +355,7 @@ __device__ __forceinline__ int32_t pick(const VerifyArgs& a, const Weights& w, d
   const int c = sm.found_chunk;
   *mine = c >= int(int64_t(chunks) * share / a.spread) &&
           c < int(int64_t(chunks) * (share + 1) / a.spread);
-  if (!*mine) return -1;
+  if (!*mine || !sv_ok(c >= 0)) return -1;
   double v[kVec];
   const int64_t v0 = int64_t(c) * kChunk + tid * kVec;
   Probs probs;
@@ -412,6 +414,7 @@ __global__ __launch_bounds__(kBlock) void verify_kernel(VerifyArgs a) {
   const int tid = int(threadIdx.x), lane = tid % kWave;
   const Nodes nd = nodes_of(a.node_start, b, a.T, a.max_nodes);
   const int n = nd.n < 0 ? 0 : nd.n;
+  if (!sv_ok(b < a.B && nd.first + n <= a.T)) return;
   int bits = nd.n < 0 ? SV_ERR_TREE : 0;
 
   // What the walk needs of every node: its parent, token, uniform, and its
@@ -507,6 +510,11 @@ __global__ __launch_bounds__(kBlock) void verify_kernel(VerifyArgs a) {
         // nothing left by rounding: from the target's row itself
         w = Weights{w.p, nullptr, 0.0, 0, 0};
       }
+      if (!sv_ok(cur < n && (a.spread == 1 ||
+                             sums + a.chunks <= a.sums + (b + 1) * (a.max_nodes + 1) * a.chunks))) {
+        bits |= SV_ERR_ROW;
+        break;
+      }
       bool here = held_node == cur;
       mass = mass_of<DT, VEC, KEEP>(a, w, sums, share, sm, held, here);
       held_node = here ? cur : -1;
@@ -521,6 +529,7 @@ __global__ __launch_bounds__(kBlock) void verify_kernel(VerifyArgs a) {
   }
   const bool none = n == 0 || bits != 0;
   if (!mine || tid >= kWave) return;
+  if (!sv_ok(taken < a.max_path)) return;
   int32_t* path = a.path + b * a.max_path;
   int32_t* emitted = a.emitted ? a.emitted + b * a.max_path : nullptr;
   for (int i = lane; i < a.max_path; i += kWave) {
@@ -556,6 +565,10 @@ bool sizes_ok(int64_t B, int64_t V, int64_t max_nodes) {
 }
 
 }  // namespace
+
+#ifdef SV_DEVICE_CHECKS
+bool sv_add_tree_verify_checks(uint32_t* count, int reset) { return sv_add_checks(count, reset); }
+#endif
 
 extern "C" {
 
@@ -595,7 +608,7 @@ int specverify_tree_verify(const void* target_probs, const void* draft_probs, in
   uint64_t* sums = static_cast<uint64_t*>(workspace);
   VerifyArgs a{target_probs, draft_probs, t_stride, d_stride, tokens, parents, node_start, u, r, T,
                V, int(max_nodes), int(max_path), mode, spread, int(chunks), sums, accept_len, path,
-               emitted, out_token, device_error};
+               emitted, out_token, device_error, B};
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   if (spread > 1) {
     const int64_t words = B * (max_nodes + 1) * chunks, blocks = (words + 1023) / 1024;

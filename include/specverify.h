@@ -405,7 +405,8 @@ int specverify_time_next_stream_kernel(void* before, void* after);
  * Debugging aid. A library built with device-side index checks
  * (build.py --checked: libspecverify_checked.so, -DSV_DEVICE_CHECKS) has every
  * work unit of every kernel check the indices it derived (batch row, branch,
- * position, chunk, split, accept length) against the sizes it was launched
+ * position, chunk, split, accept length; request, node, page, slot, share and
+ * tile of the operators on drafted trees) against the sizes it was launched
  * with before touching memory; a failed check is counted on the device and
  * the unit is skipped. This call copies the count of the current device into
  * *count and, when reset is non-zero, sets it to zero. Blocking (a device copy
