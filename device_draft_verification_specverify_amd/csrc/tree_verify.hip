@@ -38,6 +38,17 @@ constexpr uint64_t kPatience = 2000;
 constexpr uint64_t kEmpty = ~uint64_t(0);           // a sum not yet there
 constexpr uint64_t kWrong = 0xFFF8000000000001ull;  // the chunk holds what is no probability
 
+// In the build with index checks every second workgroup of a request finds runs
+// of the others' sums missing, in some groups taken at once all, in some a few:
+// what a workgroup does that has waited in vain runs wherever several share a row.
+__device__ __forceinline__ bool in_vain(int share, int chunk) {
+#ifdef SV_DEVICE_CHECKS
+  return share % 2 == 1 && chunk / 6 % 2 == 0;
+#else
+  return false;
+#endif
+}
+
 struct VerifyArgs {
   const void* p;
   const void* q;
@@ -304,6 +315,7 @@ __device__ __forceinline__ double mass_of(const VerifyArgs& a, const Weights& w,
         __builtin_amdgcn_s_sleep(1);
         s = __hip_atomic_load(sums + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
+      if (in_vain(share, c)) s = kEmpty;
       missing = missing || s == kEmpty;
       sm.front[c] = __longlong_as_double((long long)s);
     }

@@ -408,7 +408,8 @@ int specverify_time_next_stream_kernel(void* before, void* after);
  * position, chunk, split, accept length; request, node, page, slot, share and
  * tile of the operators on drafted trees) against the sizes it was launched
  * with before touching memory; a failed check is counted on the device and
- * the unit is skipped. This call copies the count of the current device into
+ * the unit is skipped. In this build some workgroups of specverify_tree_verify
+ * act as if others had been late, so that they take those sums themselves. This call copies the count of the current device into
  * *count and, when reset is non-zero, sets it to zero. Blocking (a device copy
  * on the null stream): call after the work to be checked has completed.
  * Status: SV_ENOCHECKS in a build without the checks (the product library),

@@ -1,5 +1,7 @@
 """GPU: the operators on drafted trees in the build with device-side index checks, loaded beside the
-product library: no check may fail, and the results are the product's."""
+product library. No check may fail; verification there also takes the way of a workgroup that has
+waited for the others' sums in vain (every second workgroup of a request finds some of them
+missing), and has to give the product's results all the same."""
 from __future__ import annotations
 
 import ctypes
@@ -12,6 +14,7 @@ import torch
 import device_draft_verification_specverify_amd as sv
 import test_gpu_tree_attention as att
 import test_gpu_tree_cache as cache
+import test_gpu_tree_draw as draw
 import test_gpu_tree_verify as ver
 from device_draft_verification_specverify_amd import build
 from oracle import tree as ora
@@ -40,6 +43,37 @@ def checked(monkeypatch):
             monkeypatch.setattr(sv, "_lib", product)
 
     return on_checked
+
+
+# several workgroups a request: rows in registers, rows read again (64 requests, or shares of more
+# chunks than a workgroup takes at once), rows that begin anywhere
+@pytest.mark.parametrize("mode", ver.MODES)
+@pytest.mark.parametrize("B,most,V,stride", [(3, 20, 40000, None), (5, 12, 128256, None),
+                                             (64, 4, 40000, None), (40, 6, 60000, None),
+                                             (3, 9, 40000, 40003), (2, 7, 300000, None)])
+def test_verification_without_the_others_sums(checked, mode, B, most, V, stride):
+    c = ver.case(B + V + mode, B, most, "random", V, mode)
+    want = ver.check(c, stride=stride)
+    got = checked(lambda: ver.run(c, stride=stride))
+    for k in ("accept_len", "path", "emitted", "out_token"):
+        assert np.array_equal(got[k], want[k]), k
+    assert got["error"] == want["error"]
+
+
+def test_draws_without_the_others_sums(checked):
+    c = draw.stars(7, 64, 128256, 20, 2, ora.IID)
+    want = ver.check(c)
+    assert np.array_equal(checked(lambda: ver.run(c))["out_token"], want["out_token"])
+
+
+def test_wrong_rows_without_the_others_sums(checked):
+    c = ver.case(9, 6, 5, "chain", 60000, ora.IID)
+    c["target"][c["node_start"][1], 50000] = float("nan")
+    c["draft"][c["node_start"][3], 100] = -1.0
+    want = ver.check(c)
+    got = checked(lambda: ver.run(c))
+    assert got["error"] == want["error"]
+    assert np.array_equal(got["accept_len"], want["accept_len"])
 
 
 @pytest.mark.parametrize("mode", ver.MODES)
