@@ -1061,12 +1061,12 @@ int specverify_tree_attention(
   const int64_t k31 = int64_t(1) << 31;
   if (!pow2(page_size) || page_size >= k31 || max_pages < 1 || max_pages >= k31 ||
       max_pages * page_size + max_nodes > k31 - (1 << 14) || num_pages < 1 || num_pages >= k31 ||
-      table_stride < max_pages)
+      table_stride < max_pages || !stride_ok(table_stride))
     return SV_EINVAL;
   const int64_t strides[] = {q_stride_t, q_stride_h, n_stride_t, n_stride_h, c_stride_page,
                              c_stride_token, c_stride_h, o_stride_t, o_stride_h};
   for (int64_t s : strides)
-    if (s < 0) return SV_EINVAL;
+    if (!stride_ok(s)) return SV_EINVAL;
   if (!(scale > 0.0f) || !std::isfinite(scale * kLog2e)) return SV_EINVAL;
   if (dtype != SV_BF16 && dtype != SV_F16) return SV_EDTYPE;
   for (int64_t s : strides)

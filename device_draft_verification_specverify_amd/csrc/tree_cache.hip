@@ -259,7 +259,7 @@ int specverify_tree_plan(const int32_t* parents, const int32_t* node_start,
   if (!pow2(page_size) || !under31(page_size) || max_pages < 1 || !under31(max_pages) ||
       num_pages < 1 || !under31(num_pages) || num_free < 0 || !under31(num_free) ||
       !under31(B * max_pages) || !under31(max_pages * page_size + max_nodes) ||
-      table_stride < max_pages)
+      table_stride < max_pages || !stride_ok(table_stride))
     return SV_EINVAL;
   if (pages_out == pages_in || free_head_out == free_head_in) return SV_EINVAL;
   PlanArgs a{parents,   node_start,   prefix_len, pages_in, block_table, free_pages, free_head_in,
@@ -293,7 +293,7 @@ int specverify_tree_commit(const void* k_tree, const void* v_tree, void* k_cache
   const int64_t strides[] = {n_stride_l, n_stride_t, n_stride_h,    c_stride_l,
                              c_stride_page, c_stride_token, c_stride_h};
   for (int64_t s : strides)
-    if (s < 0) return SV_EINVAL;
+    if (!stride_ok(s)) return SV_EINVAL;
   if (dtype != SV_F32 && dtype != SV_BF16 && dtype != SV_F16) return SV_EDTYPE;
   const int64_t esz = dtype == SV_F32 ? 4 : 2;
   for (int64_t s : strides)

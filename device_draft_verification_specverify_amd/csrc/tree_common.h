@@ -23,6 +23,10 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 inline bool pow2(int64_t x) { return x >= 1 && (x & (x - 1)) == 0; }
 
+// Strides in elements. No memory holds rows that lie further apart, and below it a
+// stride in bytes cannot overflow.
+inline bool stride_ok(int64_t x) { return x >= 0 && x < (int64_t(1) << 48); }
+
 inline int log2_of(int64_t x) { return 63 - __builtin_clzll(uint64_t(x)); }
 
 inline bool workspace_ok(const void* ws, size_t have, size_t need, int* status) {

@@ -604,7 +604,7 @@ int specverify_tree_verify(const void* target_probs, const void* draft_probs, in
     return SV_EINVAL;
   if (mode == SV_DRAFT_FIXED ? draft_probs != nullptr : (T > 0 && !draft_probs)) return SV_EINVAL;
   if (!sizes_ok(B, V, max_nodes) || T < 0 || T >= (int64_t(1) << 31) || max_path < 1 ||
-      max_path > max_nodes || t_stride < 0 || d_stride < 0)
+      max_path > max_nodes || !stride_ok(t_stride) || !stride_ok(d_stride))
     return SV_EINVAL;
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_EDTYPE;
   int st = SV_OK;

@@ -31,7 +31,8 @@
  * Pages
  * -----
  * - The cache of a layer is [num_pages, page_size, heads, D] with D contiguous
- *   and any other strides (in elements, >= 0); page_size is a power of two.
+ *   and any other strides; page_size is a power of two. Strides are in elements
+ *   here and everywhere, 0 <= stride < 2^48.
  *   Position i of request b is at slot block_table[b, i / page_size] *
  *   page_size + i % page_size.
  *
@@ -104,7 +105,7 @@ extern "C" {
  * or position with T = 0; B < 1, T < 0, max_nodes outside [1, 128], max_path
  * outside [1, max_nodes], page_size no power of two, max_pages, num_pages < 1
  * or num_free < 0 or any of them >= 2^31, B * max_pages or max_pages * page_size
- * + max_nodes >= 2^31, table_stride < max_pages, pages_out or free_head_out that
+ * + max_nodes >= 2^31, table_stride < max_pages or no stride, pages_out or free_head_out that
  * is pages_in or free_head_in), SV_EHIP.
  */
 int specverify_tree_plan(const int32_t* parents, const int32_t* node_start,
@@ -159,8 +160,8 @@ size_t specverify_tree_attention_workspace_size(int64_t B, int64_t T, int64_t Hq
  * D no multiple of 8 or outside [8, 256], max_nodes outside [1, 128],
  * max_nodes * Hq / Hkv > 2^16, B * Hkv > 2^24, page_size no power of two,
  * max_pages < 1 or max_pages * page_size + max_nodes > 2^31 - 2^14, T * Hq >= 2^31,
- * num_pages < 1, negative stride, rows of out that overlap, table_stride <
- * max_pages, scale), SV_EDTYPE, SV_EALIGN (q, k, v, cache or out pointers or
+ * num_pages < 1, a stride below 0 or from 2^48 on, rows of out that overlap,
+ * table_stride < max_pages, scale), SV_EDTYPE, SV_EALIGN (q, k, v, cache or out pointers or
  * strides not multiples of 16 bytes), SV_EWORKSPACE, SV_EHIP.
  */
 int specverify_tree_attention(
@@ -221,7 +222,7 @@ size_t specverify_tree_verify_workspace_size(int64_t B, int64_t V, int64_t max_n
  * Status: SV_EINVAL (null pointer but emitted, device_error or, with T = 0, the
  * [T, ...] arrays; draft_probs missing or, for SV_DRAFT_FIXED, given; unknown
  * mode; B < 1, T < 0, V outside [1, 2^22], max_nodes outside [1, 128], max_path
- * outside [1, max_nodes], negative stride), SV_EDTYPE, SV_EWORKSPACE,
+ * outside [1, max_nodes], a stride below 0 or from 2^48 on), SV_EDTYPE, SV_EWORKSPACE,
  * SV_EALIGN (workspace), SV_EHIP.
  */
 int specverify_tree_verify(const void* target_probs, const void* draft_probs, int dtype, int mode,
@@ -253,7 +254,7 @@ int specverify_tree_verify(const void* target_probs, const void* draft_probs, in
  * layers, B, H < 1, T < 0, D no multiple of 8 or outside [8, 256], max_nodes
  * outside [1, 128], max_path outside [1, max_nodes], num_pages < 1, page_size no
  * power of two, num_pages * page_size >= 2^40, layers * B >= 2^31, H >= 2^16,
- * negative stride, tokens of the cache that overlap), SV_EDTYPE, SV_EALIGN
+ * a stride below 0 or from 2^48 on, tokens of the cache that overlap), SV_EDTYPE, SV_EALIGN
  * (pointers or strides of nodes or cache not multiples of 16 bytes), SV_EHIP.
  */
 int specverify_tree_commit(const void* k_tree, const void* v_tree, void* k_cache, void* v_cache,
