@@ -16,11 +16,12 @@
 //
 // What bounds it, heads of 128 in bf16: for few rows memory, with a ring of tiles
 // in LDS kept full over the ends of items (64 single tokens over 1000 to 16000 keys
-// 414 us, 5.4 TB/s; 64 chains of 9 over 301 to 8011 keys 231 us, 4.8 TB/s); for
-// many rows each wavefront's own chain of LDS reads, products and exponentials
-// (16 trees of 64 nodes, 256 rows an item: 198 us, 3.0 TB/s and 0.56 PFLOP/s; per
-// 64 keys fetch 0.6 us, K Q 0.5, softmax 0.4, P V 0.64, barrier 0.6); for a few
-// hundred keys latency (one token over 500: 18 us).
+// 407 us, 5.5 TB/s; 64 chains of 9 over 301 to 8011 keys 231 us, 4.8 TB/s); for
+// many rows each wavefront's own chain of fetches, LDS reads, products and
+// exponentials (16 trees of 64 nodes, 256 rows an item: 197 us, 3.0 TB/s and 0.56
+// PFLOP/s; per 64 keys fetch 0.6 us, K Q 0.5, softmax 0.4, P V 0.64, barrier 0.6);
+// for a few hundred keys latency (one token over 100 keys, one tile, 12 us; over
+// 500 keys, four tiles, 17.5 us: 10 us whatever the keys, 1.8 us a tile).
 
 #include "tree_common.h"
 
@@ -81,7 +82,7 @@ struct AttnArgs {
   // workspace
   struct Split* split;  // [workers], and all tiles in one more's start
   float* part;          // [workers * 2][M][DP + 4]: sums, then m and l
-  int tile_keys, tile_rows, width, whole;
+  int tile_keys, tile_rows, whole;
 };
 
 // An item (request, key head, row tile) that a worker began inside of: its tiles
@@ -143,9 +144,10 @@ __device__ __forceinline__ Req uniform_request(Args a, int64_t b) {
 // for each of its tiles and kItemPlaces more for what it costs besides (rows
 // loaded, wavefronts joined, results written).
 // Where no request can have many tiles and every item has a worker, items are not
-// split (`whole`): one place each, and nothing to join (32 requests of up to 600
-// tokens: 24 us so, 30 us split; one token over 500 keys 20 and 22 us; 256
-// requests, with 8 items a worker, 170 us so, 147 us split).
+// split (`whole`): one place each, and nothing to join (calls, both sides timed
+// together: 32 requests of up to 600 tokens 24 us so, 30 us split; one token over
+// 500 keys 20 and 22 us; 256 requests, with 8 items a worker, 170 us so, 147 us
+// split).
 constexpr int kWorkers = 256;  // one to a CU
 constexpr int kItemPlaces = 3;
 constexpr int kWholeTiles = 6;
@@ -712,6 +714,11 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
       for (int st = 0; st < STEPS; ++st) {
         const int hb = st / PER, db0 = st % PER * (STEP / 2);
         if (st + 1 < STEPS) read_v((st + 1) / PER, (st + 1) % PER * (STEP / 2), vf[(st + 1) % 2]);
+        // The weights are rounded to the storage type here, the product's operands
+        // being of 16 bits: each is off by at most half a step of it (2^-8 in bf16),
+        // an output by that times sum p |v|. Their sum l keeps the float32 ones.
+        // A second product for what the rounding takes away would add half to the
+        // matrix work of a tile.
         typename E::vec pf;
 #pragma unroll
         for (int j = 0; j < 8; ++j) pf[j] = elem(s[hb / 2][8 * (hb % 2) + j]);
@@ -971,6 +978,8 @@ __global__ __launch_bounds__(kWorkers) void join_kernel(AttnArgs a) {
 //   more: 16 trees of 64 nodes 222 us, 243 us in two tiles of 128 rows
 // Heads wider than 128 (registers for 4 wavefronts): 64 rows 110 us, 125 us with the
 // kernel of 128 rows; 16 rows 187 and 200 us, 269 us with one of 32.
+// (Each pair was timed together, some before later steps made both sides faster;
+// the head of this file has the present times.)
 struct Variant {
   int rw, kw, kb, width;
 };
@@ -1123,7 +1132,6 @@ int specverify_tree_attention(
                                     align256(size_t(kWorkers + 1) * sizeof(Split)));
   a.tile_keys = v.kw * v.kb;
   a.tile_rows = 32 * v.rw;
-  a.width = v.width;
   const int64_t items = B * Hkv * ((max_nodes * (Hq / Hkv) + a.tile_rows - 1) / a.tile_rows);
   a.whole = max_pages * page_size + max_nodes <= kWholeTiles * int64_t(a.tile_keys) &&
             items <= kWorkers;

@@ -14,9 +14,13 @@
 //
 // What bounds it is the chain of those passes: one is 1 MB of two float32 rows at
 // V = 128256, about 4 us with its sums gathered from 8 workgroups, and none can
-// begin before the one before has decided. 64 chains of 9 nodes (one or two
-// passes each, 66 MB of rows) take 24 us; 24 trees of 33 nodes 36 us; one chain
-// at V = 32000 13 us, most of it trips to memory that wait for each other.
+// begin before the one before has decided: 24 trees of 33 nodes 36 us. A chain
+// takes one pass, for the rejected child or at its end (a second one only if
+// rounding leaves no weight). 64 chains of 9 nodes take 15.5 us at V = 32768, 16 us
+// at 65536 and 24 us at 128256, where 66 MB of rows would take 14 us; one chain at
+// V = 32000 13.5 us. So a walk of one pass costs some 13 us whatever the rows: trips to
+// memory that wait for each other (the request, its tokens, their probabilities, the
+// rows, the other workgroups' sums, the drawn chunk again).
 
 #include "tree_common.h"
 
