@@ -17,6 +17,10 @@ SOURCE = os.path.join(HERE, "csrc", "specverify.hip")
 # The operators on drafted token trees, a translation unit each.
 TREE_SOURCES = [os.path.join(HERE, "csrc", n)
                 for n in ("tree_cache.hip", "tree_verify.hip", "tree_attention.hip")]
+# The operators around a verification step, a translation unit each.
+SERVING_SOURCES = [os.path.join(HERE, "csrc", n)
+                   for n in ("serving_pages.hip", "serving_rotate.hip", "serving_attention.hip",
+                             "serving_logits.hip")]
 HOST_SOURCES = [os.path.join(HERE, "csrc", "bandit.cpp")]
 INCLUDE = os.path.join(ROOT, "include")
 LIBRARY = os.path.join(HERE, "libspecverify.so")
@@ -67,7 +71,7 @@ def build(verbose: bool = False, extra_flags: list[str] | None = None,
     with tempfile.TemporaryDirectory() as d:
         # one compiler per source, side by side, then one link
         units = [(src, os.path.join(d, os.path.basename(src) + ".o"))
-                 for src in [SOURCE, *TREE_SOURCES, *HOST_SOURCES]]
+                 for src in [SOURCE, *TREE_SOURCES, *SERVING_SOURCES, *HOST_SOURCES]]
         compile_flags = [f for f in flags if f != "-shared"]
         cmds = [[hipcc(), *compile_flags, "-I", INCLUDE, "-c", src, "-o", obj]
                 for src, obj in units]

@@ -33,6 +33,10 @@ static inline bool sv_add_checks(uint32_t* count, int reset) {
 SV_HIDDEN bool sv_add_tree_cache_checks(uint32_t* count, int reset);
 SV_HIDDEN bool sv_add_tree_verify_checks(uint32_t* count, int reset);
 SV_HIDDEN bool sv_add_tree_attention_checks(uint32_t* count, int reset);
+SV_HIDDEN bool sv_add_serving_attention_checks(uint32_t* count, int reset);
+SV_HIDDEN bool sv_add_serving_logits_checks(uint32_t* count, int reset);
+SV_HIDDEN bool sv_add_serving_pages_checks(uint32_t* count, int reset);
+SV_HIDDEN bool sv_add_serving_rotate_checks(uint32_t* count, int reset);
 #else
 #define sv_ok(ok) true
 #endif

@@ -1,0 +1,358 @@
+// serving_logits.hip -- penalties for repeated tokens, biases and grammar masks on
+// the logits of drafted nodes (gfx950).
+//
+// A workgroup takes kChunk ids of a request: what the request's history says of them
+// is counted into LDS once, for all its rows, and each row adds the tokens of its
+// own path to it while it passes. So the history is read once for each chunk (out of
+// the L2) and the logits once.
+
+#include "specverify_serving.h"
+#include "tree_common.h"
+
+namespace {
+
+using namespace svtree;
+
+constexpr int kBlock = 512;
+constexpr int kVec = 8;
+constexpr int kChunk = kBlock * kVec;  // 4096 ids
+
+struct PenalizeArgs {
+  const char* logits;
+  char* out;
+  const int32_t* tokens;
+  const int32_t* node_start;
+  const uint64_t* anc;
+  const int32_t* history;
+  const int32_t* prefix_len;
+  const int32_t* prompt_len;
+  const float* repetition;
+  const float* presence;
+  const float* frequency;
+  const int32_t* bias_start;
+  const int32_t* bias_token;
+  const float* bias;
+  const uint8_t* mask;
+  int64_t B, T, V, max_history, num_bias, history_stride;
+  int64_t row, out_row, mask_row;  // bytes
+  int max_nodes, words, chunks;
+  int32_t* err;
+};
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void load8(const char* row, int64_t v, int64_t V, float (&x)[kVec]) {
+  if (VEC && v + kVec <= V) {
+    if constexpr (DT == SV_BF16) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(row + v * 2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(row + v * 4 + 16 * j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[4 * j + i] = __uint_as_float(w[i]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      x[i] = 0.0f;
+      if (v + i >= V) continue;
+      if constexpr (DT == SV_BF16)
+        x[i] = __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(row)[v + i]) << 16);
+      else
+        x[i] = reinterpret_cast<const float*>(row)[v + i];
+    }
+  }
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void store8(char* row, int64_t v, int64_t V, const float (&x)[kVec]) {
+  if constexpr (DT == SV_BF16) {
+    typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+    b8 y;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) y[i] = __bf16(x[i]);
+    if (VEC && v + kVec <= V) {
+      *reinterpret_cast<u32x4*>(row + v * 2) = __builtin_bit_cast(u32x4, y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        if (v + i < V) reinterpret_cast<__bf16*>(row)[v + i] = y[i];
+    }
+  } else if (VEC && v + kVec <= V) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      u32x4 w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(x[4 * j + i]);
+      *reinterpret_cast<u32x4*>(row + v * 4 + 16 * j) = w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      if (v + i < V) reinterpret_cast<float*>(row)[v + i] = x[i];
+  }
+}
+
+template <int DT, int OT, bool VEC>
+__global__ __launch_bounds__(kBlock) void penalize_kernel(PenalizeArgs a) {
+  // of each id: twice the times it was emitted, and 1 if it is in the prompt
+  __shared__ __align__(16) uint32_t seen[kChunk];
+  __shared__ __align__(16) float biases[kChunk];
+  __shared__ int32_t tok[SV_MAX_TREE_NODES];
+  __shared__ uint64_t near[2];  // nodes whose token is among the chunk's ids
+  __shared__ uint32_t biased[kChunk / 32], again[kChunk / 32];  // ids with a bias, with several
+  const int64_t b = int64_t(blockIdx.x) / a.chunks;
+  const int chunk = int(int64_t(blockIdx.x) % a.chunks);
+  const int tid = int(threadIdx.x);
+  if (!sv_ok(b < a.B)) return;
+  const bool speaks = chunk == 0 && blockIdx.y == 0;  // reports the request's errors
+  const Nodes nd = nodes_of(a.node_start, b, a.T, a.max_nodes);
+  if (nd.n <= 0 || int(blockIdx.y) >= nd.n) {
+    if (nd.n < 0 && speaks && tid == 0) set_error(a.err, SV_ERR_TREE);
+    return;
+  }
+  const int64_t v0 = int64_t(chunk) * kChunk, mine = v0 + tid * kVec;
+  const float rep = a.repetition[b], pres = a.presence[b], freq = a.frequency[b];
+  int bits = 0;
+  bool wrong = false;
+  if (!(rep > 0.0f)) {
+    bits |= SV_ERR_PENALTY;
+    wrong = true;
+  }
+  int64_t lo = 0, hi = 0;
+  if (a.bias_start) {
+    lo = a.bias_start[b];
+    hi = a.bias_start[b + 1];
+    if (lo < 0 || hi < lo || hi > a.num_bias) {
+      bits |= SV_ERR_LENGTH;
+      wrong = true;
+    }
+  }
+  if (wrong) {  // no logits: NaN
+    float x[kVec];
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) x[i] = NAN;
+    for (int i = int(blockIdx.y); i < nd.n; i += int(gridDim.y))
+      if (mine < a.V) store8<OT, VEC>(a.out + (nd.first + i) * a.out_row, mine, a.V, x);
+    if (speaks && tid == 0) set_error(a.err, bits);
+    return;
+  }
+  const auto clamped = [&](int64_t x, int64_t most) {
+    if (x < 0 || x > most) bits |= SV_ERR_LENGTH;
+    return int32_t(x < 0 ? 0 : x > most ? most : x);
+  };
+  const int32_t len = clamped(a.prefix_len[b], a.max_history);
+  const int32_t prompt = clamped(a.prompt_len[b], a.max_history);
+
+  for (int i = tid; i < kChunk; i += kBlock) seen[i] = 0;
+  if (hi > lo) {
+    for (int i = tid; i < kChunk; i += kBlock) biases[i] = 0.0f;
+    if (tid < kChunk / 32) biased[tid] = again[tid] = 0;
+  }
+  if (tid < 128) {
+    const int32_t x = tid < nd.n && sv_ok(nd.first + tid < a.T) ? a.tokens[nd.first + tid] : 0;
+    tok[tid] = x;
+    if (tid < nd.n && (x < 0 || x >= a.V)) bits |= SV_ERR_TOKEN;
+    const uint64_t in = __ballot(tid < nd.n && x >= v0 && x < v0 + kChunk && x < a.V);
+    if (tid % kWave == 0) near[tid / kWave] = in;
+  }
+  __syncthreads();
+  const int32_t* history = a.history + b * a.history_stride;
+  constexpr int AHEAD = 4;
+  for (int32_t j0 = tid; j0 < len; j0 += kBlock * AHEAD) {
+    int32_t x[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int64_t j = int64_t(j0) + u * kBlock;
+      x[u] = j < len ? history[j] : -1;
+      if (j < len && (x[u] < 0 || x[u] >= a.V)) bits |= SV_ERR_TOKEN;
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int64_t d = x[u] - v0;
+      if (d < 0 || d >= kChunk || x[u] >= a.V) continue;
+      if (j0 + u * kBlock < prompt) atomicOr(seen + d, 1u);
+      else atomicAdd(seen + d, 2u);
+    }
+  }
+  if (hi > lo) {
+    for (int64_t j = lo + tid; j < hi; j += kBlock) {
+      const int32_t x = a.bias_token[j];
+      const int64_t d = x - v0;
+      if (x < 0 || x >= a.V) bits |= SV_ERR_TOKEN;
+      if (d < 0 || d >= kChunk || x >= a.V) continue;
+      const uint32_t bit = 1u << (d & 31);
+      if (atomicOr(biased + d / 32, bit) & bit) atomicOr(again + d / 32, bit);
+    }
+    __syncthreads();
+    for (int64_t j = lo + tid; j < hi; j += kBlock) {
+      const int32_t x = a.bias_token[j];
+      const int64_t d = x - v0;
+      if (d < 0 || d >= kChunk || x >= a.V) continue;
+      float sum = a.bias[j];
+      if (again[d / 32] >> (d & 31) & 1) {
+        // several (seldom): the first one's thread adds them up, in their order
+        bool first = true;
+        for (int64_t i = lo; i < j && first; ++i) first = a.bias_token[i] != x;
+        if (!first) continue;
+        for (int64_t i = j + 1; i < hi; ++i)
+          if (a.bias_token[i] == x) sum += a.bias[i];
+      }
+      biases[d] = sum;
+    }
+  }
+  __syncthreads();
+
+  const float inv = 1.0f / rep;
+  uint64_t had[2] = {0, 0};  // the nodes that `seen` counts now
+  for (int i = int(blockIdx.y); i < nd.n; i += int(gridDim.y)) {
+    const int64_t r = nd.first + i;
+    if (!sv_ok(r < a.T)) break;
+    // the nodes of this row's path whose tokens are here
+    uint64_t on[2];
+    if (a.anc) {
+      on[0] = a.anc[r * a.words];
+      on[1] = a.words > 1 ? a.anc[r * a.words + 1] : 0;
+      on[0] &= nd.n >= 64 ? ~uint64_t(0) : (uint64_t(1) << nd.n) - 1;
+    } else {
+      on[0] = i >= 63 ? ~uint64_t(0) : (uint64_t(2) << i) - 1;
+      on[1] = i < 64 ? 0 : i >= 127 ? ~uint64_t(0) : (uint64_t(2) << (i - 64)) - 1;
+    }
+    on[0] &= near[0];
+    on[1] &= near[1];
+    if (on[0] != had[0] || on[1] != had[1]) {  // (the same for the whole workgroup)
+      __syncthreads();
+      if (tid < 128) {
+        const int change = int(on[tid / 64 & 1] >> (tid & 63) & 1) - int(had[tid / 64 & 1] >> (tid & 63) & 1);
+        if (change) atomicAdd(seen + (tok[tid] - v0), uint32_t(2 * change));
+      }
+      __syncthreads();
+      had[0] = on[0];
+      had[1] = on[1];
+    }
+    if (mine < a.V) {
+      float x[kVec];
+      load8<DT, VEC>(a.logits + r * a.row, mine, a.V, x);
+      const u32x4 c0 = *reinterpret_cast<const u32x4*>(seen + tid * kVec);
+      const u32x4 c1 = *reinterpret_cast<const u32x4*>(seen + tid * kVec + 4);
+      const u32x4 any = c0 | c1;
+      if (any[0] | any[1] | any[2] | any[3]) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          const uint32_t c = e < 4 ? c0[e] : c1[e - 4];
+          const float turned = x[e] > 0.0f ? x[e] * inv : x[e] * rep;
+          x[e] = c ? turned : x[e];
+          const float less = x[e] - fmaf(freq, float(c >> 1), pres);
+          x[e] = c > 1 ? less : x[e];
+        }
+      }
+      if (hi > lo) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) x[e] += biases[tid * kVec + e];
+      }
+      if (a.mask) {
+        const uint32_t keep = a.mask[r * a.mask_row + mine / 8];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) x[e] = keep >> e & 1 ? x[e] : -INFINITY;
+      }
+      store8<OT, VEC>(a.out + r * a.out_row, mine, a.V, x);
+    }
+  }
+  if (bits && speaks) set_error(a.err, bits);
+}
+
+template <int DT, int OT>
+void launch(const PenalizeArgs& a, bool vec, dim3 grid, hipStream_t st) {
+  if (vec) hipLaunchKernelGGL((penalize_kernel<DT, OT, true>), grid, dim3(kBlock), 0, st, a);
+  else hipLaunchKernelGGL((penalize_kernel<DT, OT, false>), grid, dim3(kBlock), 0, st, a);
+}
+
+}  // namespace
+
+#ifdef SV_DEVICE_CHECKS
+bool sv_add_serving_logits_checks(uint32_t* count, int reset) { return sv_add_checks(count, reset); }
+#endif
+
+extern "C" {
+
+int specverify_penalize(const void* logits, int dtype, const int32_t* tokens,
+                        const int32_t* node_start, const uint64_t* ancestors,
+                        const int32_t* history, const int32_t* prefix_len,
+                        const int32_t* prompt_len, const float* repetition, const float* presence,
+                        const float* frequency, const int32_t* bias_start,
+                        const int32_t* bias_token, const float* bias, const int32_t* mask,
+                        int64_t B, int64_t T, int64_t V, int64_t max_nodes, int64_t max_history,
+                        int64_t num_bias, int64_t stride, int64_t out_stride,
+                        int64_t history_stride, int64_t mask_stride, void* out, int out_dtype,
+                        int32_t* device_error, void* stream) {
+  const int64_t k31 = int64_t(1) << 31;
+  if (!node_start || !history || !prefix_len || !prompt_len || !repetition || !presence || !frequency)
+    return SV_EINVAL;
+  if (T > 0 && (!logits || !tokens || !out)) return SV_EINVAL;
+  const bool has_bias = bias_start != nullptr;
+  if (has_bias != (bias_token != nullptr) || has_bias != (bias != nullptr)) return SV_EINVAL;
+  if (B < 1 || B > (1 << 20) || T < 0 || T >= k31 || V < 1 || V > SV_MAX_TREE_VOCAB ||
+      max_nodes < 1 || max_nodes > SV_MAX_TREE_NODES || max_history < 1 || max_history >= k31 ||
+      num_bias < 0 || num_bias >= k31)
+    return SV_EINVAL;
+  if (!stride_ok(stride) || !stride_ok(out_stride) || !stride_ok(history_stride) ||
+      out_stride < V || history_stride < max_history)
+    return SV_EINVAL;
+  if (mask && (!stride_ok(mask_stride) || mask_stride < (V + 31) / 32)) return SV_EINVAL;
+  if ((dtype != SV_F32 && dtype != SV_BF16) || (out_dtype != SV_F32 && out_dtype != SV_BF16))
+    return SV_EDTYPE;
+  if (T > 0 && out == logits && (dtype != out_dtype || stride != out_stride)) return SV_EINVAL;
+  if (T == 0) return SV_OK;
+  PenalizeArgs a{};
+  const int size = dtype == SV_F32 ? 4 : 2, out_size = out_dtype == SV_F32 ? 4 : 2;
+  a.logits = static_cast<const char*>(logits);
+  a.out = static_cast<char*>(out);
+  a.tokens = tokens;
+  a.node_start = node_start;
+  a.anc = ancestors;
+  a.history = history;
+  a.prefix_len = prefix_len;
+  a.prompt_len = prompt_len;
+  a.repetition = repetition;
+  a.presence = presence;
+  a.frequency = frequency;
+  a.bias_start = bias_start;
+  a.bias_token = bias_token;
+  a.bias = bias;
+  a.mask = reinterpret_cast<const uint8_t*>(mask);
+  a.B = B;
+  a.T = T;
+  a.V = V;
+  a.max_history = max_history;
+  a.num_bias = num_bias;
+  a.history_stride = history_stride;
+  a.row = stride * size;
+  a.out_row = out_stride * out_size;
+  a.mask_row = mask_stride * 4;
+  a.max_nodes = int(max_nodes);
+  a.words = int((max_nodes + 63) / 64);
+  a.chunks = int((V + kChunk - 1) / kChunk);
+  a.err = device_error;
+  // Rows that begin at multiples of 16 bytes take 128-bit accesses.
+  const bool vec = aligned16(logits) && aligned16(out) && a.row % 16 == 0 && a.out_row % 16 == 0;
+  // A request's rows are shared out where its chunks alone leave the card idle.
+  const int64_t work = B * a.chunks;
+  int64_t split = 1024 / work;
+  if (split > max_nodes) split = max_nodes;
+  if (split < 1) split = 1;
+  const dim3 grid{unsigned(work), unsigned(split), 1u};
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (dtype == SV_F32 && out_dtype == SV_F32) launch<SV_F32, SV_F32>(a, vec, grid, st);
+  else if (dtype == SV_F32) launch<SV_F32, SV_BF16>(a, vec, grid, st);
+  else if (out_dtype == SV_F32) launch<SV_BF16, SV_F32>(a, vec, grid, st);
+  else launch<SV_BF16, SV_BF16>(a, vec, grid, st);
+  return launch_status();
+}
+
+}  // extern "C"

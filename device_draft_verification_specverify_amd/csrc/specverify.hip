@@ -3175,7 +3175,10 @@ int specverify_check_count(uint32_t* count, int reset) {
   if (!count) return SV_EINVAL;
   uint32_t sum = 0;
   if (!sv_add_checks(&sum, reset) || !sv_add_tree_cache_checks(&sum, reset) ||
-      !sv_add_tree_verify_checks(&sum, reset) || !sv_add_tree_attention_checks(&sum, reset))
+      !sv_add_tree_verify_checks(&sum, reset) || !sv_add_tree_attention_checks(&sum, reset) ||
+      !sv_add_serving_attention_checks(&sum, reset) ||
+      !sv_add_serving_logits_checks(&sum, reset) || !sv_add_serving_pages_checks(&sum, reset) ||
+      !sv_add_serving_rotate_checks(&sum, reset))
     return SV_EHIP;
   *count = sum;
   return SV_OK;
