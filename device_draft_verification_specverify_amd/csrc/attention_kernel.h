@@ -164,7 +164,9 @@ __device__ __forceinline__ Req request(const AttnArgs& a, int64_t b, int* bits =
   const int64_t len = a.prefix_len[b];
   if constexpr (CHUNK) {
     r = chunk_request(a.max_keys, a.G, a.tile_keys, a.tokens, a.rows_from, a.rows_to, r, len);
-    if (bits) *bits |= (nd.n < 0 ? SV_ERR_TREE : 0) | (r.len != len ? SV_ERR_LENGTH : 0);
+    if (bits)
+      *bits |= (nd.n < 0 ? SV_ERR_TREE : 0) |
+               (r.len != len || nd.n > a.max_keys ? SV_ERR_LENGTH : 0);
     return r;
   }
   r.len = int32_t(len < 0 ? 0 : len > a.max_keys ? a.max_keys : len);
