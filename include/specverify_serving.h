@@ -86,7 +86,9 @@ size_t specverify_pages_resize_workspace_size(int64_t B, int64_t num_pages);
  * or than the block table: SV_ERR_LENGTH) or a wrong chunk (SV_ERR_TREE) keeps
  * what it owns and gets position and slots -1. An entry outside [0, num_pages)
  * that is given back is passed by; one that is taken or that a slot needs gives
- * entry and slot -1 (SV_ERR_PAGE). Rows outside every chunk get position and slots -1.
+ * entry and slot -1 (SV_ERR_PAGE). Rows outside every chunk get position and slots -1;
+ * a row that a wrong chunk_start gives to several requests is the last one's. A
+ * *free_head_in outside [0, num_free] is taken as num_free (SV_ERR_PAGE).
  * The _out arrays must not be the _in arrays.
  * Status: SV_EINVAL (null pointer but chunk_start, shares, device_error or, with
  * T = 0, position and slots; chunk_start NULL with T > 0; B outside [1, 2^16], T < 0

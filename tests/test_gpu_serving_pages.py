@@ -52,6 +52,34 @@ def test_a_list_that_does_not_reach():
     assert np.all(got["slots"][c["chunk_start"][1]:c["chunk_start"][2]] == -1)
 
 
+def test_wrong_data_in_a_large_cache():
+    # more pages than one workgroup goes through, the same mistakes
+    c = pages_case(12, [40, 30, 50, 700], [5, 40, 7, 300], 16, spare=20000)
+    resize_check(c)
+    resize_check(dict(c, prefix_len=np.array([40, -1, 50, 700])), error=64)
+    resize_check(dict(c, chunk_start=np.array([0, 5, 3, 20, 300])), error=8)
+    resize_check(dict(c, chunk_start=np.array([0, 5, 45, 53, 10])), error=8)
+    table = c["block_table"].copy()
+    table[0, 2], table[2, 0] = -1, c["num_pages"]
+    resize_check(dict(c, block_table=table, prefix_len=np.array([0, 30, 0, 0]), chunk_start=np.array([0, 0, 300, 300, 352])), error=16)
+    free = c["free_pages"].copy()
+    free[c["free_head"] + 3] = -1
+    resize_check(dict(c, free_pages=free), error=16)
+    for head in (-1, len(free) + 1):
+        resize_check(dict(c, free_head=head), error=16)
+    resize_check(dict(c, free_head=len(free) - 21), error=16)
+    resize_check(dict(c, free_head=1, prefix_len=np.zeros(4, int), chunk_start=np.zeros(5, int), rows=0), error=16)
+
+
+def test_pages_that_come_free_are_taken_in_a_large_cache():
+    # takes that lie in several blocks of pages, some from what came free and some from the list
+    n = [9000, 12000, 64, 0]
+    c = pages_case(13, n, [0, 1000, 9500, 3000], 1, spare=5000, ended=(0,))
+    resize_check(c)
+    c = pages_case(14, n, [0, 100, 12500, 3000], 1, spare=4000, ended=(0,), shared=[(1, 0, 5000)])
+    resize_check(c, error=16)
+
+
 @pytest.mark.parametrize("B,num", [(1, 9000), (600, 40000), (65536, 70000)])
 def test_large_batches_and_caches(B, num):
     rng = np.random.default_rng(B)
