@@ -39,34 +39,43 @@ struct PenalizeArgs {
   int32_t* err;
 };
 
+// 8 logits as they are stored, and the mask's bits of them.
+template <int DT>
+struct Eight {
+  u32x4 w[DT == SV_BF16 ? 1 : 2];
+  uint32_t keep;
+};
+
 template <int DT, bool VEC>
-__device__ __forceinline__ void load8(const char* row, int64_t v, int64_t V, float (&x)[kVec]) {
+__device__ __forceinline__ Eight<DT> load8(const char* row, int64_t v, int64_t V) {
+  constexpr int N = DT == SV_BF16 ? 1 : 2;
+  Eight<DT> r;
   if (VEC && v + kVec <= V) {
-    if constexpr (DT == SV_BF16) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(row + v * 2);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(row + v * 4 + 16 * j);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[4 * j + i] = __uint_as_float(w[i]);
-      }
-    }
+    for (int j = 0; j < N; ++j) r.w[j] = *reinterpret_cast<const u32x4*>(row + v * (2 * N) + 16 * j);
   } else {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      x[i] = 0.0f;
-      if (v + i >= V) continue;
-      if constexpr (DT == SV_BF16)
-        x[i] = __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(row)[v + i]) << 16);
-      else
-        x[i] = reinterpret_cast<const float*>(row)[v + i];
+      if constexpr (DT == SV_BF16) {
+        const uint32_t x = v + i < V ? reinterpret_cast<const uint16_t*>(row)[v + i] : 0;
+        if (i % 2 == 0) r.w[0][i / 2] = x;
+        else r.w[0][i / 2] |= x << 16;
+      } else {
+        r.w[i / 4][i % 4] = v + i < V ? reinterpret_cast<const uint32_t*>(row)[v + i] : 0;
+      }
     }
+  }
+  return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void widen(const Eight<DT>& r, float (&x)[kVec]) {
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    if constexpr (DT == SV_BF16)
+      x[i] = __uint_as_float(i % 2 ? r.w[0][i / 2] & 0xFFFF0000u : r.w[0][i / 2] << 16);
+    else
+      x[i] = __uint_as_float(r.w[i / 4][i % 4]);
   }
 }
 
@@ -150,6 +159,20 @@ __global__ __launch_bounds__(kBlock) void penalize_kernel(PenalizeArgs a) {
   const int32_t len = clamped(a.prefix_len[b], a.max_history);
   const int32_t prompt = clamped(a.prompt_len[b], a.max_history);
 
+  // The first rows are on their way while the history is counted.
+  const int step = int(gridDim.y);
+  const auto fetch = [&](int i) {
+    Eight<DT> r{};
+    if (i < nd.n && mine < a.V && sv_ok(nd.first + i < a.T)) {
+      r = load8<DT, VEC>(a.logits + (nd.first + i) * a.row, mine, a.V);
+      r.keep = a.mask ? a.mask[(nd.first + i) * a.mask_row + mine / 8] : 0xFFu;
+    }
+    return r;
+  };
+  constexpr int ROWS = 3;
+  Eight<DT> ahead[ROWS];
+#pragma unroll
+  for (int u = 0; u < ROWS; ++u) ahead[u] = fetch(int(blockIdx.y) + u * step);
   for (int i = tid; i < kChunk; i += kBlock) seen[i] = 0;
   if (hi > lo) {
     for (int i = tid; i < kChunk; i += kBlock) biases[i] = 0.0f;
@@ -211,9 +234,13 @@ __global__ __launch_bounds__(kBlock) void penalize_kernel(PenalizeArgs a) {
 
   const float inv = 1.0f / rep;
   uint64_t had[2] = {0, 0};  // the nodes that `seen` counts now
-  for (int i = int(blockIdx.y); i < nd.n; i += int(gridDim.y)) {
+  for (int i = int(blockIdx.y); i < nd.n; i += step) {
     const int64_t r = nd.first + i;
     if (!sv_ok(r < a.T)) break;
+    const Eight<DT> now = ahead[0];
+#pragma unroll
+    for (int u = 0; u + 1 < ROWS; ++u) ahead[u] = ahead[u + 1];
+    ahead[ROWS - 1] = fetch(i + ROWS * step);
     // the nodes of this row's path whose tokens are here
     uint64_t on[2];
     if (a.anc) {
@@ -238,7 +265,7 @@ __global__ __launch_bounds__(kBlock) void penalize_kernel(PenalizeArgs a) {
     }
     if (mine < a.V) {
       float x[kVec];
-      load8<DT, VEC>(a.logits + r * a.row, mine, a.V, x);
+      widen<DT>(now, x);
       const u32x4 c0 = *reinterpret_cast<const u32x4*>(seen + tid * kVec);
       const u32x4 c1 = *reinterpret_cast<const u32x4*>(seen + tid * kVec + 4);
       const u32x4 any = c0 | c1;
@@ -256,11 +283,8 @@ __global__ __launch_bounds__(kBlock) void penalize_kernel(PenalizeArgs a) {
 #pragma unroll
         for (int e = 0; e < kVec; ++e) x[e] += biases[tid * kVec + e];
       }
-      if (a.mask) {
-        const uint32_t keep = a.mask[r * a.mask_row + mine / 8];
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) x[e] = keep >> e & 1 ? x[e] : -INFINITY;
-      }
+      for (int e = 0; e < kVec; ++e) x[e] = now.keep >> e & 1 ? x[e] : -INFINITY;
       store8<OT, VEC>(a.out + r * a.out_row, mine, a.V, x);
     }
   }
