@@ -25,6 +25,8 @@
 // 500 keys, four tiles, 17.5 us: 10 us whatever the keys, 1.8 us a tile).
 #pragma once
 
+#include <type_traits>
+
 #include "tree_common.h"
 
 namespace {
@@ -316,8 +318,9 @@ struct Seg {
 };
 
 // RW wavefronts along the rows (32 each), KW along a tile's keys (KB each), a
-// ring of S tiles.
-template <int DT, int DP, int RW, int KW, int KB, int S, bool CHUNK>
+// ring of S tiles. DC > 0: the wavefronts take turns (below), with DC columns of
+// the DP that a tile holds.
+template <int DT, int DP, int RW, int KW, int KB, int S, bool CHUNK, int DC = 0>
 __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   using E = Elem<DT>;
   using elem = typename E::type;
@@ -339,10 +342,12 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   __shared__ __align__(1024) char tile[S * STAGE];
   __shared__ float merge_ml[KW][RW][2][32];
   __shared__ int64_t scan[NT / 64];
-  __shared__ Seg segs[S + 2];
+  constexpr int SEGS = S + (DC ? 4 : 2);
+  __shared__ Seg segs[SEGS];
   __shared__ Cursor cursors[2];
   __shared__ int32_t id_box[NT / 64][2][64];
   __shared__ int wild_seg;
+  __shared__ int wild_of[DC ? SEGS : 1];  // the same of each share on its way
   const Args args = (Args)__builtin_amdgcn_kernarg_segment_ptr();
   const int tid = int(threadIdx.x), lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -357,6 +362,8 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   if (tid == 0) {
     a.split[w].tiles = 0;
     wild_seg = -1;
+    if constexpr (DC)
+      for (int i = 0; i < SEGS; ++i) wild_of[i] = -1;
   }
   // All tiles, and those in front of this thread's request (of the last round).
   int64_t total = 0, mine = 0, lo = 0;
@@ -568,7 +575,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
     if (one_page && cached > 0) load_lds4(id_place(table, sg.t0, cached), id_at + 256);
     turn ^= 1;
     if (tid == 0) {
-      segs[prepared % (S + 2)] = sg;
+      segs[prepared % SEGS] = sg;
       cursors[turn] = Cursor{at, b, b_first, rq, head, rt, place};
     }
     ++prepared;
@@ -579,7 +586,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
     const bool fresh = f_t == f_t1;
     if (fresh) {
       if (!more) return false;
-      const Seg& sg = segs[f_seg % (S + 2)];
+      const Seg& sg = segs[f_seg % SEGS];
       ++f_seg;
       f_t = uniform(sg.t0);
       f_t1 = uniform(sg.t1);
@@ -679,7 +686,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   uint64_t next_see0 = 0, next_see1 = 0;
   auto load_rows = [&](int which) __attribute__((always_inline)) {
     const Args s = again(args);
-    const Seg& sg = segs[which % (S + 2)];
+    const Seg& sg = segs[which % SEGS];
     if constexpr (CHUNK) {
       const int rows = uniform(sg.rows), heads = uniform(sg.heads), row0 = rw * 32;
       if (row0 >= rows) return;
@@ -727,12 +734,344 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
     asm volatile("" : "+v"(next_see0), "+v"(next_see1));
   };
 
+  // Zeros for the wild values of keys first .. keys - 1 among tile t's at tv; thread
+  // `who` of THREADS; whether there were any of its part.
+  auto tame_some = [&](char* tv, int tile_t, int who, auto threads, int first, int keys)
+                       __attribute__((always_inline)) {
+    constexpr int THREADS = decltype(threads)::value;
+    bool mine = false;
+#pragma unroll
+    for (int u = 0; u < KT * CPR / THREADS; ++u) {
+      const int unit = u * THREADS + who;
+      const int key = tile_t * KT + unit / CPR;
+      if (key >= first && key < keys) {
+        u32x4* at16 = reinterpret_cast<u32x4*>(tv + unit * 16);
+        u32x4 x = *at16;
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t lo = E::wild(x[i]) ? 0xFFFFu : 0, hi = E::wild(x[i] >> 16) ? ~0xFFFFu : 0;
+          any = any || lo || hi;
+          x[i] &= ~(lo | hi);
+        }
+        if (any) *at16 = x;
+        mine = mine || any;
+      }
+    }
+    return mine;
+  };
+  auto tame = [&](char* tv, int who, int first, int keys) __attribute__((always_inline)) {
+    return tame_some(tv, t, who, std::integral_constant<int, NT>{}, first, keys);
+  };
+
+  // What was zeroed, for the rows that see it (rare, so scores are simply taken again).
+  auto add_wild = [&](const Seg& sg) __attribute__((always_inline)) {
+    const Args s = again(args);
+    const int t0 = uniform(sg.t0), t1 = uniform(sg.t1), h = uniform(sg.h);
+    const int64_t first = uniform(sg.first);
+    // The wild values of the nodes among this share's keys, for the rows that
+    // see them (rare, so scores are simply taken again).
+    const int32_t* pages = reinterpret_cast<const int32_t*>(uniform(sg.table));
+    const int x0 = CHUNK ? all_see - len : 0;
+    for (int x = max(t0 * KT - len, x0); x < min(t1 * KT - len, n); ++x) {
+      const bool see = row_ok && (CHUNK ? x <= node : (x < 64 ? see0 >> (x & 63) : see1 >> (x & 63)) & 1);
+      const char* kp;
+      if constexpr (CHUNK) {
+        const int at = len + x;
+        const int32_t id = pages[sv_ok(at < a.max_keys) ? at >> page_shift : 0];
+        if (uint32_t(id) >= num_pages) continue;
+        kp = reinterpret_cast<const char*>(uniform(sg.head)) + id * c_page +
+             (at & in_page) * c_token;
+      } else {
+        kp = s->k_tree + (first + x) * s->n_t + h * s->n_h;
+      }
+      const elem* kx = reinterpret_cast<const elem*>(kp);
+      const elem* qx =
+          reinterpret_cast<const elem*>(s->q + (first + node) * s->q_t + hq * s->q_h);
+      const uint16_t* vx = reinterpret_cast<const uint16_t*>(kp + (CHUNK ? v_cache : s->v_tree));
+      float dot = 0.0f;
+#pragma unroll 1
+      for (int d = 0; d < s->D; ++d) dot = fmaf(float(qx[d]), float(kx[d]), dot);
+      // a weight that underflows is still one
+      const float px = fmaxf(__builtin_amdgcn_exp2f(fmaf(dot, s->scale_log2, -m)), 1e-30f);
+#pragma unroll
+      for (int i = 0; i < ND; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int d = i * 32 + 8 * (j / 4) + 4 * half + j % 4;
+          const uint16_t raw = d < s->D ? vx[d] : 0;
+          const float sum = fmaf(px, float(__builtin_bit_cast(elem, raw)), acc[i][j]);
+          acc[i][j] = (see & E::wild(raw)) ? sum : acc[i][j];
+          __builtin_amdgcn_sched_barrier(0);  // few registers rather than many loads at once
+        }
+    }
+  };
+  // A share's results: the item's rows, or its part of them for the join.
+  auto write_out = [&](const Seg& sg) __attribute__((always_inline)) {
+    const Args s = again(args);
+    const int t0 = uniform(sg.t0), h = uniform(sg.h);
+    const int64_t first = uniform(sg.first);
+    const bool whole = t0 == 0 && uniform(sg.t1) == uniform(sg.tiles);
+    constexpr int COLS = DC ? DC / 32 : ND;
+    if (row_ok && sv_ok(first + node < s->T && hq < s->Hq)) {
+      if (whole) {
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        char* op = s->out + (first + node) * s->o_t + hq * s->o_h + 8 * half;
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) {
+          if (i % KW != kw) continue;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (i * 32 + 8 * j >= s->D) continue;  // D is a multiple of 8
+            typedef elem e4 __attribute__((ext_vector_type(4)));
+            e4 x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = elem(acc[i][4 * j + k] * inv);
+            *reinterpret_cast<e4*>(op + (i * 32 + 8 * j) * 2) = x;
+          }
+        }
+        if (s->lse && half == 0 && kw == 0)
+          s->lse[(first + node) * s->Hq + hq] =
+              l > 0.0f || l != l ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+      } else {
+        // a share of the keys: slot 0 of the worker if it began inside the
+        // item (its first), slot 1 if it ends inside (its last)
+        float* p = s->part + ((w * 2 + (t0 > 0 ? 0 : 1)) * M + rw * 32 + col) * int64_t(DP + 4);
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) {
+          if (i % KW != kw) continue;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<f32x4*>(p + i * 32 + 8 * j + 4 * half) =
+                f32x4{acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]};
+        }
+        if (half == 0 && kw == 0) {
+          p[DP] = m;
+          p[DP + 1] = l;
+        }
+      }
+    }
+    if (t0 > 0 && tid == 0)
+      s->split[w] = CHUNK ? Split{sg.start, first + sg.token0, sg.tiles, h, sg.heads, sg.rows}
+                          : Split{sg.start, first, sg.tiles, h, sg.rt * M, n * s->G};
+  };
   prepare();
   meet();
   if (more) load_rows(0);
   rows_here();
   asm volatile("s_waitcnt vmcnt(0)" : : : "memory");  // the first page ids
   int fetched = 0, done = 0;
+  if constexpr (DC > 0) {
+    // Many rows: two halves of the workgroup, one wavefront of each to a SIMD, take
+    // turns. While one half has the matrix cores (O += V P of the tile before, S = K Q
+    // of this one) the other takes the softmax of its scores on the vector units, and
+    // a barrier changes them over: with all 8 wavefronts in step each unit waits for
+    // the other. Both ask for the tile two ahead when the stage of the tile two before
+    // has been read by both.
+    //   phase 2 i:      first half products of tile i, second half softmax of i - 1
+    //   phase 2 i + 1:  first half softmax of i, second half products of i
+    // A tile's loads have from phase 2 (i - 2) to the end of 2 i - 1 to land.
+    static_assert(CHUNK && KW == 1 && NB == 2 && S == 4, "whole rows, 64 keys a tile");
+    constexpr int KS = DC / 16, COLS = DC / 32, NV = 4 * COLS, NK = 2 * KS;
+#ifndef VR
+#define VR 8
+#define VS 4
+#endif
+    constexpr int R = VR, STEPS = VS;  // fragments read ahead, products between reads
+    const bool second = wv >= RW / 2;
+    auto change = [&]() __attribute__((always_inline)) {
+      __builtin_amdgcn_sched_barrier(0);
+      meet();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto fetch = [&]() __attribute__((always_inline)) {
+      if (fetch_next(fetched % S)) ++fetched;
+    };
+    // this wavefront's part of tile x is here
+    auto landed = [&](int x) __attribute__((always_inline)) {
+      if (fetched > x + 1) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(LOADS) : "memory");
+      else asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    };
+    typename E::vec pf[4];
+    // Products: of the tile before's values, stage `before`, and of this one's keys.
+    auto products = [&](f32x16 (&s)[2], uint32_t before, uint32_t now, auto from, auto to)
+                        __attribute__((always_inline)) {
+      constexpr int F0 = decltype(from)::value, F1 = decltype(to)::value;
+      auto fragment = [&](int f) __attribute__((always_inline)) {
+        if (f < NV) {
+          const uint32_t at = (before + v_off) ^ ((f % COLS) * 64);
+          const uint32_t rows = f / COLS * 16 * (DP * 2);
+          const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s16x4*)(at + rows));
+          const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s16x4*)((at ^ 32) + rows + 8 * (DP * 2)));
+          return __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+        const int g = f - NV;
+        return *reinterpret_cast<__attribute__((address_space(3))) const s16x8*>(
+            ((now + k_off) ^ (g / 2 * 32)) + g % 2 * 32 * (DP * 2));
+      };
+      s16x8 b[R];
+#pragma unroll
+      for (int f = 0; f < R; ++f) b[f] = fragment(F0 + f);
+      if constexpr (F1 > NV) {
+        s[0] = f32x16{0};
+        s[1] = f32x16{0};
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int f0 = F0; f0 < F1; f0 += STEPS) {
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j) {
+          const int f = f0 + j;
+          const s16x8 x = b[(f - F0) % R];
+          if (f < NV) acc[f % COLS] = E::mfma(x, pf[f / COLS], acc[f % COLS]);
+          else s[(f - NV) % 2] = E::mfma(x, __builtin_bit_cast(typename E::vec, qf[(f - NV) / 2]), s[(f - NV) % 2]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j)
+          if (f0 + j + R < F1) b[(f0 + j - F0) % R] = fragment(f0 + j + R);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    auto values = [&](uint32_t before) __attribute__((always_inline)) {
+      f32x16 none[2];
+      products(none, before, 0, std::integral_constant<int, 0>{}, std::integral_constant<int, NV>{});
+    };
+    auto finish = [&](int which) __attribute__((always_inline)) {
+      const Seg& sg = segs[which % SEGS];
+      l += __shfl_xor(l, 32);
+      if (wild_of[which % SEGS] == which) add_wild(sg);
+      write_out(sg);
+    };
+
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      fetch();
+      meet();
+    }
+    if (fetched == 0) return;  // its places are none of tiles
+    landed(0);
+    meet();
+    if (second) {
+      fetch();
+      change();
+    }
+#pragma unroll
+    for (int hb = 0; hb < 4; ++hb) pf[hb] = typename E::vec{};
+#pragma unroll
+    for (int i = 0; i < ND; ++i) acc[i] = f32x16{0};
+    bool act = false;  // whether this wavefront has rows that see the tile
+    int wave_last = 0;
+#pragma unroll 1
+    for (; done < fetched; ++done) {
+      const bool fresh = t == t1;
+      if (fresh) {
+        const Seg& sg = segs[seg % SEGS];
+        t = uniform(sg.t0);
+        t1 = uniform(sg.t1);
+        ++seg;
+        const int rows = uniform(sg.rows);
+        wave_ok = rw * 32 < rows;
+        wave_last = uniform(sg.len) + uniform(sg.token0) +
+                    (min(rows, rw * 32 + 32) - 1) / uniform(sg.heads);
+      }
+      const uint32_t now = tile_at + uint32_t(done % S) * STAGE;
+      const uint32_t before = tile_at + uint32_t((done + S - 1) % S) * STAGE;
+      const bool act_before = act;
+      f32x16 s[2];
+      act = wave_ok && t * KT <= wave_last;
+      __builtin_amdgcn_s_setprio(1);
+      // (Where it saw nothing of the tile before, its weights are zeros, and so are the
+      // values that are not finite; in front of the first tile there is anything, but no
+      // sum yet. One way through is fewer registers than three.)
+      if (act_before || act)
+        products(s, before, now, std::integral_constant<int, 0>{},
+                 std::integral_constant<int, NV + NK>{});
+      __builtin_amdgcn_s_setprio(0);
+      if (second) landed(done + 1);
+      else fetch();
+      change();
+
+      if (second) fetch();
+      if (fresh) {
+        if (done > 0) finish(seg - 2);
+        const Seg& sg = segs[(seg - 1) % SEGS];
+        len = uniform(sg.len);
+        n = uniform(sg.n);
+        const int rows = uniform(sg.rows), heads = uniform(sg.heads), r = rw * 32 + col;
+        row_ok = r < rows;
+        const int token = (row_ok ? r : 0) / heads;
+        node = uniform(sg.token0) + token;
+        hq = uniform(sg.h) + (row_ok ? r - token * heads : 0);
+        all_see = len + uniform(sg.token0) + 1;
+        last = len + node;
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) acc[i] = f32x16{0};
+        m = -INFINITY;
+        l = 0.0f;
+      }
+      if (!second && t * KT + KT > all_see)  // read by nobody before the next phase
+        if (tame_some(tile + done % S * STAGE + KT * DP * 2, t, tid,
+                      std::integral_constant<int, NT / 2>{}, all_see, len + n))
+          wild_of[(seg - 1) % SEGS] = seg - 1;
+      if (act) {
+        if (t * KT + KT > all_see) {
+          const int ahead = last - (t * KT + 4 * half);
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              s[nb][i] = nb * 32 + 8 * (i / 4) + i % 4 <= ahead ? s[nb][i] : -INFINITY;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) top = fmaxf(top, s[nb][i]);
+        top *= a.scale_log2;
+        top = fmaxf(top, __shfl_xor(top, 32));
+        // The reference may lag behind the maximum: weights up to 2^8 are as exact as
+        // those up to 1, and sums of 2^31 of them far from float32's end.
+        if (__any(top > m + 8.0f)) {
+          const float to = fmaxf(m, top);
+          const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+          l *= f;
+#pragma unroll
+          for (int i = 0; i < COLS; ++i) acc[i] *= f;
+          m = to;
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int nb = 0; nb < 2; ++nb)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            s[nb][i] = __builtin_amdgcn_exp2f(fmaf(s[nb][i], a.scale_log2, -ref));
+            l += s[nb][i];
+          }
+        // (rounded as below)
+#pragma unroll
+        for (int hb = 0; hb < 4; ++hb)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) pf[hb][j] = elem(s[hb / 2][8 * (hb % 2) + j]);
+      } else {
+#pragma unroll
+        for (int hb = 0; hb < 4; ++hb) pf[hb] = typename E::vec{};
+      }
+      if (t + 1 == t1 && fetched > done + 1) {
+        load_rows(seg);
+        rows_here();
+      }
+      if (!second) landed(done + 1);
+      change();
+      ++t;
+    }
+    if (act) values(tile_at + uint32_t((done + S - 1) % S) * STAGE);
+    finish(seg - 1);
+    if (!second) change();
+    return;
+  }
 #pragma unroll 1
   for (int i = 0; i < S - 1; ++i) {
     if (fetch_next(i)) ++fetched;
@@ -747,7 +1086,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
 
     if (t == t1) {
       const Args s = again(args);
-      const Seg& sg = segs[seg % (S + 2)];
+      const Seg& sg = segs[seg % SEGS];
       t = uniform(sg.t0);
       t1 = uniform(sg.t1);
       len = uniform(sg.len);
@@ -789,26 +1128,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
     // (A chunk's keys that the item's first token sees are seen by all its rows.)
     const int some_see = CHUNK ? all_see : len;  // keys from here on are not seen by all
     if (t * KT + KT > some_see) {
-      bool mine = false;
-#pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        const int unit = u * NT + tid;
-        const int key = t * KT + unit / CPR;
-        if (key >= some_see && key < keys) {
-          u32x4* at16 = reinterpret_cast<u32x4*>(tv + unit * 16);
-          u32x4 x = *at16;
-          bool any = false;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = E::wild(x[i]) ? 0xFFFFu : 0, hi = E::wild(x[i] >> 16) ? ~0xFFFFu : 0;
-            any = any || lo || hi;
-            x[i] &= ~(lo | hi);
-          }
-          if (any) *at16 = x;
-          mine = mine || any;
-        }
-      }
-      if (mine) wild_seg = seg;
+      if (tame(tv, tid, some_see, keys)) wild_seg = seg;
       meet();
       wild = wild_seg == seg;
     }
@@ -916,10 +1236,9 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
     if (t == t1) {
       if (fetched - done > 1) load_rows(seg);
       const Args s = again(args);
-      const Seg& sg = segs[(seg - 1) % (S + 2)];
+      const Seg& sg = segs[(seg - 1) % SEGS];
       const int t0 = uniform(sg.t0), h = uniform(sg.h);
       const int64_t first = uniform(sg.first);
-      const bool whole = t0 == 0 && t1 == uniform(sg.tiles);
       l += __shfl_xor(l, 32);
 
       if constexpr (KW > 1) {
@@ -975,86 +1294,11 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
       }
 
       if (wild) {
-        // The wild values of the nodes among this share's keys, for the rows that
-        // see them (rare, so scores are simply taken again).
-        const int32_t* pages = reinterpret_cast<const int32_t*>(uniform(sg.table));
-        const int x0 = CHUNK ? all_see - len : 0;
-        for (int x = max(t0 * KT - len, x0); x < min(t1 * KT - len, n); ++x) {
-          const bool see = row_ok && (CHUNK ? x <= node : (x < 64 ? see0 >> (x & 63) : see1 >> (x & 63)) & 1);
-          const char* kp;
-          if constexpr (CHUNK) {
-            const int at = len + x;
-            const int32_t id = pages[sv_ok(at < a.max_keys) ? at >> page_shift : 0];
-            if (uint32_t(id) >= num_pages) continue;
-            kp = reinterpret_cast<const char*>(uniform(sg.head)) + id * c_page +
-                 (at & in_page) * c_token;
-          } else {
-            kp = s->k_tree + (first + x) * s->n_t + h * s->n_h;
-          }
-          const elem* kx = reinterpret_cast<const elem*>(kp);
-          const elem* qx =
-              reinterpret_cast<const elem*>(s->q + (first + node) * s->q_t + hq * s->q_h);
-          const uint16_t* vx = reinterpret_cast<const uint16_t*>(kp + (CHUNK ? v_cache : s->v_tree));
-          float dot = 0.0f;
-#pragma unroll 1
-          for (int d = 0; d < s->D; ++d) dot = fmaf(float(qx[d]), float(kx[d]), dot);
-          // a weight that underflows is still one
-          const float px = fmaxf(__builtin_amdgcn_exp2f(fmaf(dot, s->scale_log2, -m)), 1e-30f);
-#pragma unroll
-          for (int i = 0; i < ND; ++i)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int d = i * 32 + 8 * (j / 4) + 4 * half + j % 4;
-              const uint16_t raw = d < s->D ? vx[d] : 0;
-              const float sum = fmaf(px, float(__builtin_bit_cast(elem, raw)), acc[i][j]);
-              acc[i][j] = (see & E::wild(raw)) ? sum : acc[i][j];
-              __builtin_amdgcn_sched_barrier(0);  // few registers rather than many loads at once
-            }
-        }
+        add_wild(sg);
       }
 
       rows_here();
-      if (row_ok && sv_ok(first + node < s->T && hq < s->Hq)) {
-        if (whole) {
-          const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-          char* op = s->out + (first + node) * s->o_t + hq * s->o_h + 8 * half;
-#pragma unroll
-          for (int i = 0; i < ND; ++i) {
-            if (i % KW != kw) continue;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (i * 32 + 8 * j >= s->D) continue;  // D is a multiple of 8
-              typedef elem e4 __attribute__((ext_vector_type(4)));
-              e4 x;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) x[k] = elem(acc[i][4 * j + k] * inv);
-              *reinterpret_cast<e4*>(op + (i * 32 + 8 * j) * 2) = x;
-            }
-          }
-          if (s->lse && half == 0 && kw == 0)
-            s->lse[(first + node) * s->Hq + hq] =
-                l > 0.0f || l != l ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
-        } else {
-          // a share of the keys: slot 0 of the worker if it began inside the
-          // item (its first), slot 1 if it ends inside (its last)
-          float* p = s->part + ((w * 2 + (t0 > 0 ? 0 : 1)) * M + rw * 32 + col) * int64_t(DP + 4);
-#pragma unroll
-          for (int i = 0; i < ND; ++i) {
-            if (i % KW != kw) continue;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<f32x4*>(p + i * 32 + 8 * j + 4 * half) =
-                  f32x4{acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]};
-          }
-          if (half == 0 && kw == 0) {
-            p[DP] = m;
-            p[DP + 1] = l;
-          }
-        }
-      }
-      if (t0 > 0 && tid == 0)
-        s->split[w] = CHUNK ? Split{sg.start, first + sg.token0, sg.tiles, h, sg.heads, sg.rows}
-                            : Split{sg.start, first, sg.tiles, h, sg.rt * M, n * s->G};
+      write_out(sg);
     }
     st_now = st_now + 1 == S ? 0 : st_now + 1;
     st_next = st_next + 1 == S ? 0 : st_next + 1;
@@ -1070,7 +1314,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
 // most of them without work, and a share at a time: 16.2 and 15.7 us.)
 constexpr int kJoiners = 2048;
 template <int DT, int DP, bool CHUNK>
-__global__ __launch_bounds__(kWorkers) void join_kernel(AttnArgs a) {
+__device__ __forceinline__ void join_items(const AttnArgs& a, int block, int blocks) {
   using elem = typename Elem<DT>::type;
   constexpr int LANES = DP / 4, ROWS = kWorkers / LANES, AHEAD = 4;
   __shared__ Split item;
@@ -1093,7 +1337,7 @@ __global__ __launch_bounds__(kWorkers) void join_kernel(AttnArgs a) {
     if (k < tid / kWave) upto += wave_units[k];
     all += wave_units[k];
   }
-  for (int u = int(blockIdx.x); u < all; u += int(gridDim.x)) {
+  for (int u = block; u < all; u += blocks) {
     if (u >= upto - units && u < upto) {
       item = own;
       item_second = tid;
@@ -1161,6 +1405,22 @@ __global__ __launch_bounds__(kWorkers) void join_kernel(AttnArgs a) {
     if (a.lse && d0 == 0)
       a.lse[(sp.first + node) * a.Hq + hq] =
           some ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+  }
+}
+
+template <int DT, int DP, bool CHUNK>
+__global__ __launch_bounds__(kWorkers) void join_kernel(AttnArgs a) {
+  join_items<DT, DP, CHUNK>(a, int(blockIdx.x), int(gridDim.x));
+}
+
+// Of two launches, half of the workgroups each.
+template <int DT, int DP, bool CHUNK>
+__global__ __launch_bounds__(kWorkers) void join_both_kernel(AttnArgs a, AttnArgs b) {
+  const int half = int(gridDim.x / 2), block = int(blockIdx.x);
+  if (block < half) {
+    if (!a.whole) join_items<DT, DP, CHUNK>(a, block, half);
+  } else if (!b.whole) {
+    join_items<DT, DP, CHUNK>(b, block - half, half);
   }
 }
 

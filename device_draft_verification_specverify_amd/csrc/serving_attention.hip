@@ -7,15 +7,22 @@
 
 namespace {
 
-// Which kernel: rows of the largest chunk in wavefronts of 32 rows, and the rest of a
-// workgroup along the keys, as for drafted trees.
+// Which kernel: by the rows that a request has of a key head, tokens times query
+// heads. Few of them (a single token, a short chunk) leave wavefronts of a workgroup
+// for the keys of a tile, as for drafted trees; many take all of them, and each other's
+// turns on the matrix cores. A batch may hold both: then either kernel passes the
+// other's requests by, in a launch of its own.
+constexpr int kFewRows = 64;
+
 struct Variant {
   int rw, kw, kb, width;
   int rows() const { return 32 * rw; }
+  int keys() const { return kw * kb; }
 };
+int width_of(int64_t D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 Variant variant_of(int64_t rows, int64_t D) {
   Variant v;
-  v.width = D <= 64 ? 64 : D <= 128 ? 128 : 256;
+  v.width = width_of(D);
   if (v.width == 256) {
     v.rw = rows <= 64 ? 2 : 4;
     v.kw = 4 / v.rw;
@@ -28,9 +35,9 @@ Variant variant_of(int64_t rows, int64_t D) {
   return v;
 }
 
-template <int DT, int DP, int RW, int KW, int KB, int S>
+template <int DT, int DP, int RW, int KW, int KB, int S, int DC = 0>
 void launch_one(const AttnArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((attention_kernel<DT, DP, RW, KW, KB, S, true>), dim3(unsigned(kWorkers)),
+  hipLaunchKernelGGL((attention_kernel<DT, DP, RW, KW, KB, S, true, DC>), dim3(unsigned(kWorkers)),
                      dim3(64 * RW * KW), 0, st, a);
 }
 
@@ -43,17 +50,30 @@ void launch(const Variant& v, const AttnArgs& a, hipStream_t st) {
     constexpr int X = 128 / DP;  // stages of half the size, twice as many
     if (v.rw == 2) launch_one<DT, DP, 2, 4, 32, 2 * X>(a, st);
     else if (v.rw == 4) launch_one<DT, DP, 4, 2, 64, 2 * X>(a, st);
-    else launch_one<DT, DP, 8, 1, 64, 4>(a, st);
+    else if (a.D > 96 || DP == 64) launch_one<DT, DP, 8, 1, 64, 4, DP>(a, st);
+    else if constexpr (DP == 128) launch_one<DT, DP, 8, 1, 64, 4, 96>(a, st);
   }
-  if (a.whole) return;
-  hipLaunchKernelGGL((join_kernel<DT, DP, true>), dim3(kJoiners), dim3(kWorkers), 0, st, a);
+}
+
+// few: null where one kernel takes all requests.
+template <int DT, int DP>
+void launch_both(const Variant& v, const AttnArgs& a, const AttnArgs* few, hipStream_t st) {
+  launch<DT, DP>(v, a, st);
+  if (few) {
+    launch<DT, DP>(variant_of(kFewRows, few->D), *few, st);
+    if (!a.whole || !few->whole)
+      hipLaunchKernelGGL((join_both_kernel<DT, DP, true>), dim3(2 * kJoiners), dim3(kWorkers), 0, st,
+                         a, *few);
+  } else if (!a.whole) {
+    hipLaunchKernelGGL((join_kernel<DT, DP, true>), dim3(kJoiners), dim3(kWorkers), 0, st, a);
+  }
 }
 
 template <int DT>
-void launch_width(const Variant& v, const AttnArgs& a, hipStream_t st) {
-  if (v.width == 64) launch<DT, 64>(v, a, st);
-  else if (v.width == 128) launch<DT, 128>(v, a, st);
-  else launch<DT, 256>(v, a, st);
+void launch_width(const Variant& v, const AttnArgs& a, const AttnArgs* few, hipStream_t st) {
+  if (v.width == 64) launch_both<DT, 64>(v, a, few, st);
+  else if (v.width == 128) launch_both<DT, 128>(v, a, few, st);
+  else launch_both<DT, 256>(v, a, few, st);
 }
 
 bool sizes_ok(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_chunk) {
@@ -66,6 +86,26 @@ bool sizes_ok(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t 
 // Rows of the largest chunk: no request has more than all of them.
 int64_t most_rows(int64_t T, int64_t G, int64_t max_chunk) {
   return (max_chunk < T ? max_chunk : T) * G;
+}
+
+size_t workspace_of(const Variant& v) {
+  return align256(size_t(kWorkers + 1) * sizeof(Split)) +
+         align256(size_t(kWorkers) * 2 * v.rows() * (v.width + 4) * sizeof(float));
+}
+
+// How a kernel takes the requests whose rows are from `from` to `to`.
+void take(AttnArgs& a, const Variant& v, int from, int to, int64_t most, char* workspace) {
+  a.split = reinterpret_cast<Split*>(workspace);
+  a.part = reinterpret_cast<float*>(workspace + align256(size_t(kWorkers + 1) * sizeof(Split)));
+  a.tile_keys = v.keys();
+  a.tile_rows = v.rows();
+  a.GS = a.G < a.tile_rows ? a.G : a.tile_rows;
+  a.parts = (a.G + a.GS - 1) / a.GS;
+  a.tokens = a.tile_rows / a.GS;
+  a.rows_from = from;
+  a.rows_to = to;
+  const int64_t items = a.B * a.Hkv * a.parts * ((most + a.tokens - 1) / a.tokens);
+  a.whole = a.max_keys <= kWholeTiles * int64_t(a.tile_keys) && items <= kWorkers;
 }
 
 }  // namespace
@@ -82,8 +122,7 @@ size_t specverify_chunk_attention_workspace_size(int64_t B, int64_t T, int64_t H
                                                  int64_t D, int64_t max_chunk) {
   if (!sizes_ok(B, T, Hq, Hkv, D, max_chunk)) return 0;
   const Variant v = variant_of(most_rows(T, Hq / Hkv, max_chunk), D);
-  return align256(size_t(kWorkers + 1) * sizeof(Split)) +
-         align256(size_t(kWorkers) * 2 * v.rows() * (v.width + 4) * sizeof(float));
+  return workspace_of(v) + (v.rows() > kFewRows ? workspace_of(variant_of(kFewRows, D)) : 0);
 }
 
 int specverify_chunk_attention(const void* q, const void* k_cache, const void* v_cache, int dtype,
@@ -153,22 +192,17 @@ int specverify_chunk_attention(const void* q, const void* k_cache, const void* v
   a.max_nodes = int(max_chunk);
   a.page_shift = log2_of(page_size);
   a.scale_log2 = scale * kLog2e;
-  a.split = static_cast<Split*>(workspace);
-  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                    align256(size_t(kWorkers + 1) * sizeof(Split)));
-  a.tile_keys = v.kw * v.kb;
-  a.tile_rows = v.rows();
-  a.GS = a.G < a.tile_rows ? a.G : a.tile_rows;
-  a.parts = (a.G + a.GS - 1) / a.GS;
-  a.tokens = a.tile_rows / a.GS;
-  a.rows_from = 0;
-  a.rows_to = INT_MAX;
   const int64_t most = max_chunk < T ? max_chunk : T;
-  const int64_t items = B * Hkv * a.parts * ((most + a.tokens - 1) / a.tokens);
-  a.whole = a.max_keys <= kWholeTiles * int64_t(a.tile_keys) && items <= kWorkers;
+  char* const ws = static_cast<char*>(workspace);
+  // Chunks of fewer rows beside the largest: not where one request is all there is, or
+  // all have as many tokens as the longest may have.
+  const bool mixed = v.rows() > 128 && B > 1 && T < B * most;
+  take(a, v, mixed ? kFewRows + 1 : 0, INT_MAX, most, ws);
+  AttnArgs few = a;
+  if (mixed) take(few, variant_of(kFewRows, D), 0, kFewRows, most, ws + workspace_of(v));
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  if (dtype == SV_BF16) launch_width<SV_BF16>(v, a, st);
-  else launch_width<SV_F16>(v, a, st);
+  if (dtype == SV_BF16) launch_width<SV_BF16>(v, a, mixed ? &few : nullptr, st);
+  else launch_width<SV_F16>(v, a, mixed ? &few : nullptr, st);
   return launch_status();
 }
 
