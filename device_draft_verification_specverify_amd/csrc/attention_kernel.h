@@ -86,6 +86,7 @@ struct AttnArgs {
   // chunks (below): query heads of a row tile at most, parts of a key head's query
   // heads, whole tokens of a row tile, and the rows that requests taken here have
   int GS, parts, tokens, rows_from, rows_to;
+  int item_places;  // what an item costs besides its tiles, in tiles
   // workspace
   struct Split* split;  // [workers], and all tiles in one more's start
   float* part;          // [workers * 2][M][DP + 4]: sums, then m and l
@@ -132,29 +133,26 @@ __device__ __forceinline__ int chunk_tiles(int tile_keys, int tokens, const Req&
   return (r.len + upto + tile_keys - 1) / tile_keys;
 }
 
-// sum over i < n of floor((a i + b) / m), as in Euclid's algorithm: whole parts are
-// taken out, and what is left is counted along the other axis. (a m and a n below 2^31)
-__device__ __forceinline__ int64_t floor_sum(uint32_t n, uint32_t m, uint32_t a, uint32_t b) {
-  int64_t sum = 0;
-  while (n > 0) {
-    sum += int64_t(n) * (n - 1) / 2 * (a / m) + int64_t(n) * (b / m);
-    a %= m;
-    b %= m;
-    const uint32_t y = a * n + b;
-    n = y / m;
-    b = y % m;
-    const uint32_t old = m;
-    m = a;
-    a = old;
-  }
-  return sum;
+// sum over i < n of floor((a i + b) / 2^s): the sum of a i + b without what each leaves.
+// What they leave repeats after 2^s / g of them, g the largest power of two in a up to
+// 2^s, and is each of b mod g, b mod g + g, ... once in a period; the rest of a period is
+// gone through. (Divisions, as in Euclid's algorithm, took 5 us of a call.)
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int s, uint32_t a, uint32_t b) {
+  const uint32_t m = 1u << s, low = (a & (0u - a)) | m, g = low & (0u - low);
+  const int period_log = s - (31 - __builtin_clz(g));
+  const int64_t period = int64_t(1) << period_log;
+  int64_t left = (n >> period_log) *
+                 (period * (b & (g - 1)) + int64_t(g) * (period * (period - 1) / 2));
+  const int rest = int(n & (period - 1));
+  for (int i = 0; i < rest; ++i) left += (a * uint32_t(i) + b) & (m - 1);
+  return (int64_t(a) * (n * (n - 1) / 2) + int64_t(b) * n - left) >> s;
 }
 
 // Tiles of the first k row tiles, of row_tiles at most.
 __device__ __forceinline__ int64_t chunk_tile_sum(int tile_keys, int tokens, const Req& r, int k) {
   if (k == 0) return 0;
   const int full = k < r.row_tiles ? k : k - 1;
-  return floor_sum(full, tile_keys, tokens, r.len + tokens + tile_keys - 1) +
+  return floor_sum(full, 31 - __builtin_clz(tile_keys), tokens, r.len + tokens + tile_keys - 1) +
          (full < k ? r.tiles : 0);
 }
 template <bool CHUNK>
@@ -227,14 +225,14 @@ __device__ __forceinline__ int64_t places_of(int whole, int heads, const Req& r)
   return int64_t(item_places(whole, r.tiles)) * r.row_tiles * heads;
 }
 // The same for chunks: of the first k row tiles of one part of a key head's rows.
-__device__ __forceinline__ int64_t chunk_places(int whole, int tile_keys, int tokens, const Req& r,
-                                                int k) {
-  return whole ? k : int64_t(kItemPlaces) * k + chunk_tile_sum(tile_keys, tokens, r, k);
+__device__ __forceinline__ int64_t chunk_places(const AttnArgs& a, const Req& r, int k) {
+  return a.whole ? k
+                 : int64_t(a.item_places) * k + chunk_tile_sum(a.tile_keys, a.tokens, r, k);
 }
 template <bool CHUNK>
 __device__ __forceinline__ int64_t all_places(const AttnArgs& a, const Req& r) {
   if constexpr (CHUNK)
-    return chunk_places(a.whole, a.tile_keys, a.tokens, r, r.row_tiles) * (a.Hkv * a.parts);
+    return chunk_places(a, r, r.row_tiles) * (a.Hkv * a.parts);
   else
     return places_of(a.whole, a.Hkv, r);
 }
@@ -356,7 +354,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
 
   // This worker's share: neighbours in the order of tiles share an XCD's L2
   // (workgroups go round robin over the 8 XCDs).
-  const int workers = int(gridDim.x);
+  constexpr int workers = kWorkers;
   const int64_t w = workers % 8 == 0 ? (blockIdx.x % 8) * (workers / 8) + blockIdx.x / 8
                                      : blockIdx.x;
   if (tid == 0) {
@@ -389,7 +387,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
   }
   const int64_t at = uniform(share_start(total, workers, w));
   const int64_t end = uniform(share_start(total, workers, w + 1));
-  if (!sv_ok(workers == kWorkers && w < workers && at <= end && end <= total)) return;
+  if (!sv_ok(int(gridDim.x) == workers && w < workers && at <= end && end <= total)) return;
   if (w == 0 && tid == 0) a.split[workers].start = total;
   if (at >= end) return;
   // the request that holds tile `at`: more than NT of them are gone through again
@@ -413,25 +411,34 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
       }
     }
     if (at >= lo && at < lo + mine) {
-      Cursor c{at, o + tid, lo, own, 0, 0, 0};
-      if constexpr (CHUNK) {
-        const int64_t each = mine / (a.Hkv * a.parts), into = at - lo;
-        c.head = int32_t(into / each);
-        const int64_t within = into - c.head * each;
-        int less = 0, above = own.row_tiles;  // the last row tile that begins no later
-        while (above - less > 1) {
-          const int mid = (less + above) / 2;
-          if (chunk_places(a.whole, a.tile_keys, a.tokens, own, mid) <= within) less = mid;
-          else above = mid;
-        }
-        c.rt = less;
-        c.place = int32_t(within - chunk_places(a.whole, a.tile_keys, a.tokens, own, less));
-      }
-      cursors[0] = c;
+      cursors[0] = Cursor{at, o + tid, lo, own, 0, 0, 0};
+      if constexpr (CHUNK) cursors[1].at = chunk_places(a, own, own.row_tiles);
     }
     if (base > at) break;
   }
   __syncthreads();
+  if constexpr (CHUNK) {
+    // Its part of the heads and its row tile, the one that begins last of those that
+    // begin no later: every thread tries one (512 at a time), for a sum takes long.
+    const Req rq = cursors[0].rq;
+    const int64_t each = cursors[1].at, into = at - cursors[0].b_first;
+    int head = int(double(into) / double(each));  // to one less or more
+    if (head * each > into) --head;
+    if ((head + 1) * each <= into) ++head;
+    const int64_t within = into - head * each;
+    for (int k0 = 0; k0 < rq.row_tiles; k0 += NT) {
+      const int k = k0 + tid;
+      if (k >= rq.row_tiles) break;
+      const int64_t begins = chunk_places(a, rq, k);
+      const int64_t places = a.whole ? 1 : chunk_tiles(a.tile_keys, a.tokens, rq, k) + a.item_places;
+      if (begins <= within && within < begins + places) {
+        cursors[0].head = head;
+        cursors[0].rt = k;
+        cursors[0].place = int32_t(within - begins);
+      }
+    }
+    __syncthreads();
+  }
 
   // This lane's places in a stage. K: row col, piece 2 ks + half; V: 4 keys from
   // 4 half on at 4 columns. Pieces are swizzled by their row, rows a multiple of
@@ -508,7 +515,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
           }
         }
         sg.tiles = chunk_tiles(s->tile_keys, s->tokens, rq, rt);
-        const int size = item_places(s->whole, sg.tiles);
+        const int size = s->whole ? 1 : sg.tiles + s->item_places;
         const int64_t left = end - at;
         const int upto = size - place < left ? size : place + int(left);
         sg.start = at - place;
@@ -761,7 +768,7 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
     return mine;
   };
   auto tame = [&](char* tv, int who, int first, int keys) __attribute__((always_inline)) {
-    return tame_some(tv, t, who, std::integral_constant<int, NT>{}, first, keys);
+    return tame_some(tv, t, tid, std::integral_constant<int, NT>{}, first, keys);
   };
 
   // What was zeroed, for the rows that see it (rare, so scores are simply taken again).
@@ -866,78 +873,195 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
     // turns. While one half has the matrix cores (O += V P of the tile before, S = K Q
     // of this one) the other takes the softmax of its scores on the vector units, and
     // a barrier changes them over: with all 8 wavefronts in step each unit waits for
-    // the other. Both ask for the tile two ahead when the stage of the tile two before
-    // has been read by both.
+    // the other.
     //   phase 2 i:      first half products of tile i, second half softmax of i - 1
     //   phase 2 i + 1:  first half softmax of i, second half products of i
-    // A tile's loads have from phase 2 (i - 2) to the end of 2 i - 1 to land.
-    static_assert(CHUNK && KW == 1 && NB == 2 && S == 4, "whole rows, 64 keys a tile");
+    // Tiles are asked for during the products, a load now and then between them (all at
+    // once they hold up the wavefront for longer than a third of a phase): in those of
+    // tile i the keys of i + 3, whose stage was read last in phase 2 i - 1, and the
+    // values of i + 2, alike. They are read from phase 2 i + 5 on (values that are not
+    // finite; products from 2 i + 6 on), so each wavefront sees to it that its part is
+    // here at the end of 2 i + 4, when the first half has asked for two more such batches
+    // and the second for one. Behind the last tile there are loads, too, of zeros that
+    // nobody reads, so the count of a batch is always the same.
+    static_assert(CHUNK && KW == 1 && NB == 2 && S == 4 && SAME, "whole rows, 64 keys a tile");
     constexpr int KS = DC / 16, COLS = DC / 32, NV = 4 * COLS, NK = 2 * KS;
-#ifndef VR
-#define VR 8
-#define VS 4
-#endif
-    constexpr int R = VR, STEPS = VS;  // fragments read ahead, products between reads
+    constexpr int R = 8;  // fragments read ahead
+    static_assert(R <= NV, "the first ones are of values");
     const bool second = wv >= RW / 2;
     auto change = [&]() __attribute__((always_inline)) {
       __builtin_amdgcn_sched_barrier(0);
       meet();
       __builtin_amdgcn_sched_barrier(0);
     };
-    auto fetch = [&]() __attribute__((always_inline)) {
-      if (fetch_next(fetched % S)) ++fetched;
+    // this wavefront's loads but its newest `batches` are here
+    auto landed = [&](auto batches) __attribute__((always_inline)) {
+      asm volatile("s_waitcnt vmcnt(%0)" : : "n"(decltype(batches)::value * LOADS) : "memory");
     };
-    // this wavefront's part of tile x is here
-    auto landed = [&](int x) __attribute__((always_inline)) {
-      if (fetched > x + 1) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(LOADS) : "memory");
-      else asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+    const std::integral_constant<int, 1> one_batch;
+    const std::integral_constant<int, 2> two_batches;
+
+    // This lane's pieces of the tile that was found last: its keys, its values, and the
+    // values of the one before.
+    const char *kp[UNITS], *vp[UNITS], *old_vp[UNITS];
+    const char* nothing = zero;  // (held, or it is found anew at every use)
+    asm volatile("" : "+s"(nothing));
+    const int piece = (lane % CPR) ^ swizzle<CPR>(wv * WROWS + lane_row);
+    const int64_t lane_off = lane_row * c_token + piece * 16;
+    const bool lane_ok = piece * 8 < a.D;
+    int64_t to_values = v_cache;  // (scalar registers are short)
+    asm volatile("" : "+v"(to_values));
+    // Where the rows of this wavefront's loads begin, in BATCH tiles from f_batch on, one
+    // a lane, and in which of them the page is none of the cache's.
+    uint64_t bases = 0, bad = 0;
+    int f_safe = 0;  // up to this tile all is as usual: whole tiles of good pages
+    auto take_bases = [&](int box) __attribute__((always_inline)) {
+      take_ids(box);
+      const int row = (f_batch + lane / UNITS) * KT + lane % UNITS * (NT / CPR) + wv * WROWS;
+      bad = __ballot(uint32_t(ids) >= num_pages);
+      bases = reinterpret_cast<uint64_t>(f_head) + uint32_t(ids) * uint64_t(c_page) +
+              uint32_t(row & in_page) * uint64_t(c_token);
+      if (f_batch + BATCH < f_t1) load_lds4(id_place(f_table, f_batch + BATCH, f_len), id_at);
     };
-    typename E::vec pf[4];
-    // Products: of the tile before's values, stage `before`, and of this one's keys.
-    auto products = [&](f32x16 (&s)[2], uint32_t before, uint32_t now, auto from, auto to)
-                        __attribute__((always_inline)) {
-      constexpr int F0 = decltype(from)::value, F1 = decltype(to)::value;
-      auto fragment = [&](int f) __attribute__((always_inline)) {
-        if (f < NV) {
-          const uint32_t at = (before + v_off) ^ ((f % COLS) * 64);
-          const uint32_t rows = f / COLS * 16 * (DP * 2);
-          const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (__attribute__((address_space(3))) s16x4*)(at + rows));
-          const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (__attribute__((address_space(3))) s16x4*)((at ^ 32) + rows + 8 * (DP * 2)));
-          return __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
-        const int g = f - NV;
-        return *reinterpret_cast<__attribute__((address_space(3))) const s16x8*>(
-            ((now + k_off) ^ (g / 2 * 32)) + g % 2 * 32 * (DP * 2));
-      };
-      s16x8 b[R];
+    auto next_tile = [&]() __attribute__((always_inline)) {
 #pragma unroll
-      for (int f = 0; f < R; ++f) b[f] = fragment(F0 + f);
-      if constexpr (F1 > NV) {
+      for (int u = 0; u < UNITS; ++u) old_vp[u] = vp[u];
+      auto found = [&](int id0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          const uint32_t lo = uint32_t(__builtin_amdgcn_readlane(int(bases), id0 + u));
+          const uint32_t hi = uint32_t(__builtin_amdgcn_readlane(int(bases >> 32), id0 + u));
+          kp[u] = reinterpret_cast<const char*>((uint64_t(hi) << 32 | lo) + lane_off);
+          vp[u] = kp[u] + to_values;
+          if (!full) {  // narrower heads: zeros behind them
+            kp[u] = lane_ok ? kp[u] : nothing;
+            vp[u] = lane_ok ? vp[u] : nothing;
+          }
+        }
+      };
+      // One test for what is usual (the tests one by one took as long as ten products).
+      if (__builtin_expect(f_t < f_safe, 1)) {
+        found((f_t - f_batch) * UNITS);
+        ++f_t;
+        ++fetched;
+        return;
+      }
+      const bool fresh = f_t == f_t1;
+      if (fresh) {
+        if (!more) {
+#pragma unroll
+          for (int u = 0; u < UNITS; ++u) kp[u] = vp[u] = nothing;
+          return;
+        }
+        const Seg& sg = segs[f_seg % SEGS];
+        ++f_seg;
+        f_t = uniform(sg.t0);
+        f_t1 = uniform(sg.t1);
+        f_len = uniform(sg.len) + uniform(sg.n);
+        f_head = reinterpret_cast<const char*>(uniform(sg.head));
+        f_table = reinterpret_cast<const int32_t*>(uniform(sg.table));
+        f_batch = f_t;
+        if (one_page) {
+          // its ids are older than the tiles of the share before but the first
+          if (f_tiles < S) asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+          take_bases(1);
+        }
+        f_tiles = f_t1 - f_t;
+      }
+      const int t = f_t++;
+      if (t - f_batch == BATCH) {
+        f_batch = t;
+        if (one_page) take_bases(0);
+      }
+      f_safe = one_page && bad == 0 ? min(min(f_t1, f_batch + BATCH), f_len / KT) : 0;
+      const int id0 = (t - f_batch) * UNITS;
+      const bool some = sv_ok(t * KT < f_len && f_seg <= prepared);
+      if (one_page) {
+        found(id0);
+        // the end of the keys, pages outside the cache
+        const bool wrong = bad >> id0 & ((1u << UNITS) - 1);
+        if (wrong || !some || t * KT + KT > f_len) {
+#pragma unroll
+          for (int u = 0; u < UNITS; ++u) {
+            const bool here = t * KT + u * (NT / CPR) + wv * WROWS + lane_row < f_len;
+            const bool good = !(bad >> (id0 + u) & 1);
+            const bool take = some && here && good;
+            kp[u] = take ? kp[u] : nothing;
+            vp[u] = take ? vp[u] : nothing;
+            if (wrong && here && !good) set_error(again(args)->err, SV_ERR_PAGE);
+          }
+        }
+      } else {  // pages of fewer rows than a wavefront loads
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          const int key = t * KT + u * (NT / CPR) + wv * WROWS + lane_row;
+          const bool here = key < f_len;
+          const int32_t page = f_table[(here ? key : f_len - 1) >> page_shift];
+          const bool good = uint32_t(page) < num_pages;
+          if (here && !good) set_error(again(args)->err, SV_ERR_PAGE);
+          const bool take = some && here && good && lane_ok;
+          kp[u] = take ? f_head + uint32_t(page) * uint64_t(c_page) +
+                             uint32_t(key & in_page) * uint64_t(c_token) + piece * 16
+                       : nothing;
+          vp[u] = take ? kp[u] + to_values : nothing;
+        }
+      }
+      ++fetched;
+      if (fresh) prepare();
+    };
+    auto ask = [&](int which, uint32_t k_stage, uint32_t v_stage) __attribute__((always_inline)) {
+      if (which < UNITS) load_lds16(old_vp[which], v_stage + wv * 1024 + which * NT * 16 + KT * DP * 2);
+      else load_lds16(kp[which - UNITS], k_stage + wv * 1024 + (which - UNITS) * NT * 16);
+    };
+    auto stage_of = [&](int x) __attribute__((always_inline)) {
+      return tile_at + uint32_t(x % S) * STAGE;
+    };
+
+    typename E::vec pf[4];
+    s16x8 b[R];
+    // The f-th fragment of the products: values of the tile before, stage `before`, then
+    // keys of this one.
+    auto fragment = [&](int f, uint32_t before, uint32_t now) __attribute__((always_inline)) {
+      if (f < NV) {
+        const uint32_t at = (before + v_off) ^ ((f % COLS) * 64);
+        const uint32_t rows = f / COLS * 16 * (DP * 2);
+        const s16x4 x0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)(at + rows));
+        const s16x4 x1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)((at ^ 32) + rows + 8 * (DP * 2)));
+        return __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
+      }
+      const int g = f - NV;
+      return *reinterpret_cast<__attribute__((address_space(3))) const s16x8*>(
+          ((now + k_off) ^ (g / 2 * 32)) + g % 2 * 32 * (DP * 2));
+    };
+    auto first_fragments = [&](uint32_t before) __attribute__((always_inline)) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int f = 0; f < R; ++f) b[f] = fragment(f, before, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // Those up to `end`, with a batch of loads among them.
+    auto products = [&](f32x16 (&s)[2], uint32_t before, uint32_t now, auto end, int i)
+                        __attribute__((always_inline)) {
+      constexpr int F1 = decltype(end)::value, EACH = (NV + NK) / LOADS;
+      constexpr bool ASK = F1 > NV;
+      const uint32_t k_stage = stage_of(i + 3), v_stage = stage_of(i + 2);
+      if constexpr (ASK) {
         s[0] = f32x16{0};
         s[1] = f32x16{0};
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int f0 = F0; f0 < F1; f0 += STEPS) {
-#pragma unroll
-        for (int j = 0; j < STEPS; ++j) {
-          const int f = f0 + j;
-          const s16x8 x = b[(f - F0) % R];
-          if (f < NV) acc[f % COLS] = E::mfma(x, pf[f / COLS], acc[f % COLS]);
-          else s[(f - NV) % 2] = E::mfma(x, __builtin_bit_cast(typename E::vec, qf[(f - NV) / 2]), s[(f - NV) % 2]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int j = 0; j < STEPS; ++j)
-          if (f0 + j + R < F1) b[(f0 + j - F0) % R] = fragment(f0 + j + R);
+      for (int f = 0; f < F1; ++f) {
+        const s16x8 x = b[f % R];
+        if (f < NV) acc[f % COLS] = E::mfma(x, pf[f / COLS], acc[f % COLS]);
+        else s[(f - NV) % 2] = E::mfma(x, __builtin_bit_cast(typename E::vec, qf[(f - NV) / 2]), s[(f - NV) % 2]);
+        if (f + R < F1) b[f % R] = fragment(f + R, before, now);
+        if constexpr (ASK)
+          if (f % EACH == EACH / 2 && f / EACH < LOADS) ask(f / EACH, k_stage, v_stage);
         __builtin_amdgcn_sched_barrier(0);
       }
-    };
-    auto values = [&](uint32_t before) __attribute__((always_inline)) {
-      f32x16 none[2];
-      products(none, before, 0, std::integral_constant<int, 0>{}, std::integral_constant<int, NV>{});
     };
     auto finish = [&](int which) __attribute__((always_inline)) {
       const Seg& sg = segs[which % SEGS];
@@ -946,16 +1070,27 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
       write_out(sg);
     };
 
+    // K 0, then V 0 and K 1, V 1 and K 2
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) vp[u] = nothing;
 #pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
-      fetch();
+    for (int i = 0; i < 3; ++i) {
+      next_tile();
+      if (i > 0)
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) ask(u, 0, stage_of(i - 1));
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) ask(UNITS + u, stage_of(i), 0);
       meet();
     }
-    if (fetched == 0) return;  // its places are none of tiles
-    landed(0);
+    if (fetched == 0) {  // its places are none of tiles
+      asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+      return;
+    }
+    landed(two_batches);
     meet();
     if (second) {
-      fetch();
+      landed(one_batch);
       change();
     }
 #pragma unroll
@@ -966,8 +1101,9 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
     int wave_last = 0;
 #pragma unroll 1
     for (; done < fetched; ++done) {
+      __builtin_amdgcn_s_setprio(1);
       const bool fresh = t == t1;
-      if (fresh) {
+      if (__builtin_expect(fresh, 0)) {
         const Seg& sg = segs[seg % SEGS];
         t = uniform(sg.t0);
         t1 = uniform(sg.t1);
@@ -977,25 +1113,22 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
         wave_last = uniform(sg.len) + uniform(sg.token0) +
                     (min(rows, rw * 32 + 32) - 1) / uniform(sg.heads);
       }
-      const uint32_t now = tile_at + uint32_t(done % S) * STAGE;
-      const uint32_t before = tile_at + uint32_t((done + S - 1) % S) * STAGE;
-      const bool act_before = act;
       f32x16 s[2];
       act = wave_ok && t * KT <= wave_last;
-      __builtin_amdgcn_s_setprio(1);
-      // (Where it saw nothing of the tile before, its weights are zeros, and so are the
-      // values that are not finite; in front of the first tile there is anything, but no
-      // sum yet. One way through is fewer registers than three.)
-      if (act_before || act)
-        products(s, before, now, std::integral_constant<int, 0>{},
-                 std::integral_constant<int, NV + NK>{});
+      // (on their way while the next tile is found)
+      first_fragments(stage_of(done + S - 1));
+      next_tile();
+      // (All wavefronts go this way, also those without rows here: one way is fewer
+      // registers than several. Where a wavefront saw nothing of the tile before its
+      // weights are zeros, and the values that are not finite are so, too; in front of
+      // the first tile there is anything, but no sum yet.)
+      products(s, stage_of(done + S - 1), stage_of(done), std::integral_constant<int, NV + NK>{},
+               done);
       __builtin_amdgcn_s_setprio(0);
-      if (second) landed(done + 1);
-      else fetch();
+      if (!second) landed(two_batches);
       change();
 
-      if (second) fetch();
-      if (fresh) {
+      if (__builtin_expect(fresh, 0)) {
         if (done > 0) finish(seg - 2);
         const Seg& sg = segs[(seg - 1) % SEGS];
         len = uniform(sg.len);
@@ -1012,12 +1145,12 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
         m = -INFINITY;
         l = 0.0f;
       }
-      if (!second && t * KT + KT > all_see)  // read by nobody before the next phase
+      if (__builtin_expect(!second && t * KT + KT > all_see, 0))  // read by nobody before the next phase
         if (tame_some(tile + done % S * STAGE + KT * DP * 2, t, tid,
                       std::integral_constant<int, NT / 2>{}, all_see, len + n))
           wild_of[(seg - 1) % SEGS] = seg - 1;
       if (act) {
-        if (t * KT + KT > all_see) {
+        if (__builtin_expect(t * KT + KT > all_see, 0)) {
           const int ahead = last - (t * KT + 4 * half);
 #pragma unroll
           for (int nb = 0; nb < 2; ++nb)
@@ -1031,10 +1164,11 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) top = fmaxf(top, s[nb][i]);
         top *= a.scale_log2;
-        top = fmaxf(top, __shfl_xor(top, 32));
+        const auto halves = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+        top = fmaxf(__uint_as_float(halves[0]), __uint_as_float(halves[1]));
         // The reference may lag behind the maximum: weights up to 2^8 are as exact as
         // those up to 1, and sums of 2^31 of them far from float32's end.
-        if (__any(top > m + 8.0f)) {
+        if (__builtin_expect(__any(top > m + 8.0f), 0)) {
           const float to = fmaxf(m, top);
           const float f = to == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - to);
           l *= f;
@@ -1059,17 +1193,22 @@ __global__ __launch_bounds__(64 * RW * KW) void attention_kernel(AttnArgs a) {
 #pragma unroll
         for (int hb = 0; hb < 4; ++hb) pf[hb] = typename E::vec{};
       }
-      if (t + 1 == t1 && fetched > done + 1) {
+      if (__builtin_expect(t + 1 == t1 && fetched > done + 1, 0)) {
         load_rows(seg);
         rows_here();
       }
-      if (!second) landed(done + 1);
+      if (second) landed(one_batch);
       change();
       ++t;
     }
-    if (act) values(tile_at + uint32_t((done + S - 1) % S) * STAGE);
+    if (act) {
+      f32x16 none[2];
+      first_fragments(stage_of(done + S - 1));
+      products(none, stage_of(done + S - 1), 0, std::integral_constant<int, NV>{}, 0);
+    }
     finish(seg - 1);
     if (!second) change();
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");  // no load outlives the workgroup
     return;
   }
 #pragma unroll 1
