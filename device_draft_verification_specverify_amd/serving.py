@@ -11,6 +11,7 @@ here records gradients.
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -59,6 +60,11 @@ def _lib() -> ctypes.CDLL:
     return lib
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(name: str, *sizes: int) -> int:
+    return int(getattr(_lib(), name)(*sizes))
+
+
 _call = _tree._call  # on the tensors' device, on its current stream
 
 
@@ -90,7 +96,7 @@ def specverify_pages_resize(prefix_len: torch.Tensor, pages: torch.Tensor,
 
     block_table [B, max_pages] and free_pages [at least num_pages] are updated in place, pages,
     free_head and shares come back new. A request ends by prefix_len 0 and no new tokens."""
-    lib = _lib()
+    _lib()
     dev = _device(prefix_len, "prefix_len")
     i32 = torch.int32
     B, free = prefix_len.numel(), free_pages.numel()
@@ -112,7 +118,7 @@ def specverify_pages_resize(prefix_len: torch.Tensor, pages: torch.Tensor,
     if start is not None:
         position = empty(rows, dtype=i32, device=dev)
         slots = empty(rows, dtype=torch.int64, device=dev)
-    ws = _scratch(ws, lib.specverify_pages_resize_workspace_size(B, num_pages), dev,
+    ws = _scratch(ws, _workspace_bytes("specverify_pages_resize_workspace_size", B, num_pages), dev,
                   "specverify_pages_resize_workspace_size")
     _call("specverify_pages_resize", dev, prefix_len.data_ptr(), start, pages.data_ptr(),
           block_table.data_ptr(), free_pages.data_ptr(), free_head.data_ptr(), held, B, rows,
@@ -139,7 +145,7 @@ def specverify_pages_fork(source: torch.Tensor, target: torch.Tensor, prefix_len
     source and target [forks] int32, k_cache and v_cache [layers, num_pages, page_size, H, D]
     (float32, bfloat16 or float16, last axis contiguous, other strides multiples of 16 bytes).
     block_table and the caches are updated in place, the rest comes back new."""
-    lib = _lib()
+    _lib()
     dev = _device(k_cache, "k_cache")
     cs = _pair(k_cache, v_cache, dev, 5, "k_cache and v_cache")
     layers, num_pages, page_size, H, D = k_cache.shape
@@ -160,7 +166,7 @@ def specverify_pages_fork(source: torch.Tensor, target: torch.Tensor, prefix_len
     now = empty(B, dtype=i32, device=dev)
     head = empty(1, dtype=i32, device=dev)
     held = empty(num_pages, dtype=i32, device=dev)
-    ws = _scratch(ws, lib.specverify_pages_fork_workspace_size(B, F), dev,
+    ws = _scratch(ws, _workspace_bytes("specverify_pages_fork_workspace_size", B, F), dev,
                   "specverify_pages_fork_workspace_size")
     _call("specverify_pages_fork", dev, source.data_ptr(), target.data_ptr(), prefix_len.data_ptr(),
           pages.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), free_head.data_ptr(),
@@ -256,7 +262,7 @@ def specverify_chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     contiguous, other strides multiples of 8 elements; the caches' strides agree), prefix_len [B]
     (the tokens in front) and chunk_start [B + 1] int32, max_chunk the longest chunk at most,
     scale 1 / sqrt(D) if not given."""
-    lib = _lib()
+    _lib()
     dev = _device(q, "q")
     qs = _strided(q, dev, 3, "q")
     cs = _pair(k_cache, v_cache, dev, 4, "k_cache and v_cache")
@@ -278,8 +284,8 @@ def specverify_chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     os_ = _strided(out, dev, 3, "out")
     err = _optional(device_error, torch.int32, (1,), dev, "device_error")
     lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if want_lse else None
-    ws = _scratch(ws, lib.specverify_chunk_attention_workspace_size(B, T, Hq, Hkv, D, max_chunk),
-                  dev, "specverify_chunk_attention_workspace_size")
+    ws = _scratch(ws, _workspace_bytes("specverify_chunk_attention_workspace_size", B, T, Hq, Hkv, D,
+                                       max_chunk), dev, "specverify_chunk_attention_workspace_size")
     _call("specverify_chunk_attention", dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           dt, B, T, Hq, Hkv, D, max_chunk, qs[0], qs[1], cs[0], cs[1], cs[2], num_pages, page_size,
           block_table.data_ptr(), max_pages, table_stride, prefix_len.data_ptr(),
