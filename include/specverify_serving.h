@@ -222,10 +222,8 @@ size_t specverify_chunk_attention_workspace_size(int64_t B, int64_t T, int64_t H
  *               all that the other spans; must not overlap an input
  *   lse         [T, Hq] float32 out or NULL: ln of the softmax's denominator
  * Values that a row does not see (of later tokens, in slots behind the chunk) do
- * not reach it, also when they are infinite or NaN. One of a token of the chunk
- * that a row sees becomes that row's in its column, whatever its weight; one in
- * front of the chunk makes the column of every row of its request and head
- * infinite or NaN. A page outside [0, num_pages) counts as zero keys and values
+ * not reach it, also when they are infinite or NaN; one that it sees makes its
+ * column infinite or NaN. A page outside [0, num_pages) counts as zero keys and values
  * (SV_ERR_PAGE); a prefix_len below 0 or too long for the block table with the
  * chunk behind it is clamped to what fits (SV_ERR_LENGTH). The rows of a request
  * with a wrong chunk_start, a chunk longer than max_chunk (SV_ERR_TREE) or than the
