@@ -21,6 +21,10 @@ using namespace svtree;
 constexpr int kBlock = 512;
 constexpr int kVec = 8;
 constexpr int kChunk = kBlock * kVec;  // 4096 ids
+constexpr int64_t kMaxGrid = 1 << 22;  // workgroups along x: threads there are counted in 32 bits
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 struct PenalizeArgs {
   const char* logits;
@@ -44,12 +48,17 @@ struct PenalizeArgs {
   int32_t* err;
 };
 
-// 8 logits as they are stored, and the mask's bits of them.
+// 8 logits as they are stored, the mask's bits of them, and their row's ancestors.
 template <int DT>
 struct Eight {
   u32x4 w[DT == SV_BF16 ? 1 : 2];
   uint32_t keep;
+  uint32_t on[4];
 };
+__device__ __forceinline__ uint64_t uniform64(uint32_t low, uint32_t high) {
+  return uint32_t(__builtin_amdgcn_readfirstlane(int(low))) |
+         uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(high)))) << 32;
+}
 
 template <int DT, bool VEC>
 __device__ __forceinline__ Eight<DT> load8(const char* row, int64_t v, int64_t V) {
@@ -125,10 +134,14 @@ __global__ __launch_bounds__(kBlock, 8) void penalize_kernel(PenalizeArgs a) {
   __shared__ int32_t tok[SV_MAX_TREE_NODES];
   __shared__ uint64_t near[2];  // nodes whose token is among the chunk's ids
   __shared__ uint32_t biased[kChunk / 32], again[kChunk / 32];  // ids with a bias, with several
-  const int64_t b = int64_t(blockIdx.x) / a.chunks;
-  const int chunk = int(int64_t(blockIdx.x) % a.chunks);
+  __shared__ int several;  // whether there are any of the latter
+  __shared__ __align__(16) int32_t list[kBlock];  // biases' ids and values
+  __shared__ __align__(16) float adds[kBlock];
+  const int64_t block = int64_t(blockIdx.z) * gridDim.x + blockIdx.x;
+  const int64_t b = block / a.chunks;
+  const int chunk = int(block % a.chunks);
   const int tid = int(threadIdx.x);
-  if (!sv_ok(b < a.B)) return;
+  if (b >= a.B) return;
   const bool speaks = chunk == 0 && blockIdx.y == 0;  // reports the request's errors
   const Nodes nd = nodes_of(a.node_start, b, a.T, a.max_nodes);
   if (nd.n <= 0 || int(blockIdx.y) >= nd.n) {
@@ -173,8 +186,15 @@ __global__ __launch_bounds__(kBlock, 8) void penalize_kernel(PenalizeArgs a) {
   const int step = int(gridDim.y);
   const auto fetch = [&](int i) {
     Eight<DT> r{};
-    if (i < nd.n && mine < a.V && sv_ok(nd.first + i < a.T)) {
-      r = load8<DT, VEC>(a.logits + (nd.first + i) * a.row, mine, a.V);
+    if (i >= nd.n || !sv_ok(nd.first + i < a.T)) return r;
+    if (a.anc) {
+      const uint32_t* on = reinterpret_cast<const uint32_t*>(a.anc + (nd.first + i) * a.words);
+      for (int j = 0; j < 4; ++j) r.on[j] = j < 2 * a.words ? on[j] : 0;
+    }
+    if (mine < a.V) {
+      const Eight<DT> x = load8<DT, VEC>(a.logits + (nd.first + i) * a.row, mine, a.V);
+#pragma unroll
+      for (int j = 0; j < int(sizeof(r.w) / sizeof(r.w[0])); ++j) r.w[j] = x.w[j];
       r.keep = a.mask ? a.mask[(nd.first + i) * a.mask_row + mine / 8] : 0xFFu;
     }
     return r;
@@ -184,6 +204,7 @@ __global__ __launch_bounds__(kBlock, 8) void penalize_kernel(PenalizeArgs a) {
   if (hi > lo) {
     for (int i = tid; i < kChunk; i += kBlock) biases[i] = 0.0f;
     if (tid < kChunk / 32) biased[tid] = again[tid] = 0;
+    if (tid == 0) several = 0;
   }
   if (tid < 128) {
     const int32_t x = tid < nd.n && sv_ok(nd.first + tid < a.T) ? a.tokens[nd.first + tid] : 0;
@@ -218,23 +239,51 @@ __global__ __launch_bounds__(kBlock, 8) void penalize_kernel(PenalizeArgs a) {
       if (x < 0 || x >= a.V) bits |= SV_ERR_TOKEN;
       if (d < 0 || d >= kChunk || x >= a.V) continue;
       const uint32_t bit = 1u << (d & 31);
-      if (atomicOr(biased + d / 32, bit) & bit) atomicOr(again + d / 32, bit);
+      if (atomicOr(biased + d / 32, bit) & bit) {
+        atomicOr(again + d / 32, bit);
+        several = 1;
+      } else {
+        biases[d] = a.bias[j];
+      }
     }
     __syncthreads();
-    for (int64_t j = lo + tid; j < hi; j += kBlock) {
-      const int32_t x = a.bias_token[j];
+    if (several) {
+      for (int i = tid; i < kChunk; i += kBlock)
+        if (again[i / 32] >> (i & 31) & 1) biases[i] = 0.0f;
+    }
+    // Several biases of an id are added up in their order, kBlock of the list at a time: by the
+    // first one's thread, which finds the others in LDS.
+    for (int64_t j0 = several ? lo : hi; j0 < hi; j0 += kBlock) {
+      const int64_t j = j0 + tid;
+      const int32_t x = j < hi ? a.bias_token[j] : -1;
+      const float add = j < hi ? a.bias[j] : 0.0f;
+      __syncthreads();
+      list[tid] = x;
+      adds[tid] = add;
+      __syncthreads();
       const int64_t d = x - v0;
       if (d < 0 || d >= kChunk || x >= a.V) continue;
-      float sum = a.bias[j];
       if (again[d / 32] >> (d & 31) & 1) {
-        // several (seldom): the first one's thread adds them up, in their order
+        // (in front of the wavefront's own part of the list, in it, and behind it)
+        const int own = tid & ~(kWave - 1), n = int(hi - j0 < kBlock ? hi - j0 : kBlock);
         bool first = true;
-        for (int64_t i = lo; i < j && first; ++i) first = a.bias_token[i] != x;
+#pragma unroll 4
+        for (int i = 0; i < own; i += 4) {
+          const i32x4 y = *reinterpret_cast<const i32x4*>(list + i);
+          first = first && y[0] != x && y[1] != x && y[2] != x && y[3] != x;
+        }
+        for (int i = own; i < tid; ++i) first = first && list[i] != x;
         if (!first) continue;
-        for (int64_t i = j + 1; i < hi; ++i)
-          if (a.bias_token[i] == x) sum += a.bias[i];
+        float sum = biases[d];
+#pragma unroll 4
+        for (int i = own; i < n; i += 4) {
+          const i32x4 y = *reinterpret_cast<const i32x4*>(list + i);
+          const f32x4 z = *reinterpret_cast<const f32x4*>(adds + i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum += y[e] == x ? z[e] : 0.0f;
+        }
+        biases[d] = sum;
       }
-      biases[d] = sum;
     }
   }
   __syncthreads();
@@ -244,13 +293,17 @@ __global__ __launch_bounds__(kBlock, 8) void penalize_kernel(PenalizeArgs a) {
   for (int i = int(blockIdx.y); i < nd.n; i += step) {
     const int64_t r = nd.first + i;
     if (!sv_ok(r < a.T)) break;
-    const Eight<DT> now = next;
+    Eight<DT> now = next;
+    // (here before the next one is asked for: a wait further down would be for both)
+#pragma unroll
+    for (int j = 0; j < int(sizeof(now.w) / sizeof(now.w[0])); ++j) asm volatile("" : "+v"(now.w[j]));
+    asm volatile("" : "+v"(now.keep), "+v"(now.on[0]), "+v"(now.on[1]), "+v"(now.on[2]), "+v"(now.on[3]));
     next = fetch(i + step);
     // the nodes of this row's path whose tokens are here
     uint64_t on[2];
     if (a.anc) {
-      on[0] = a.anc[r * a.words];
-      on[1] = a.words > 1 ? a.anc[r * a.words + 1] : 0;
+      on[0] = uniform64(now.on[0], now.on[1]);
+      on[1] = uniform64(now.on[2], now.on[3]);
       on[0] &= nd.n >= 64 ? ~uint64_t(0) : (uint64_t(1) << nd.n) - 1;
     } else {
       on[0] = i >= 63 ? ~uint64_t(0) : (uint64_t(2) << i) - 1;
@@ -375,7 +428,8 @@ int specverify_penalize(const void* logits, int dtype, const int32_t* tokens,
   int64_t split = 1024 / work;
   if (split > max_nodes) split = max_nodes;
   if (split < 1) split = 1;
-  const dim3 grid{unsigned(work), unsigned(split), 1u};
+  const int64_t x = work < kMaxGrid ? work : kMaxGrid;
+  const dim3 grid{unsigned(x), unsigned(split), unsigned((work + x - 1) / x)};
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (dtype == SV_F32 && out_dtype == SV_F32) launch<SV_F32, SV_F32>(a, vec, grid, st);
   else if (dtype == SV_F32) launch<SV_F32, SV_BF16>(a, vec, grid, st);

@@ -586,8 +586,9 @@ __global__ __launch_bounds__(kOne) void fork_plan_kernel(ForkArgs a) {
 // of the first layer writes the target's table too. 64 forks of some 16 tokens in 32
 // layers (245 MB): 50 us, 4.9 TB/s.
 __global__ __launch_bounds__(kBlock) void fork_copy_kernel(ForkArgs a) {
-  const int64_t j = int64_t(blockIdx.x) % a.forks, layer = int64_t(blockIdx.x) / a.forks;
-  if (!sv_ok(layer < a.layers)) return;
+  const int64_t block = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
+  const int64_t j = block % a.forks, layer = block / a.forks;
+  if (layer >= a.layers) return;
   const int32_t* plan = a.plans + 4 * j;
   const int32_t len = plan[0], old_page = plan[1], new_page = plan[2], place = plan[3];
   if (len < 0) return;
@@ -811,8 +812,12 @@ int specverify_pages_fork(const int32_t* source, const int32_t* target,
   const int64_t copiers = (copied + kOne * 4 - 1) / (kOne * 4);
   hipLaunchKernelGGL(fork_plan_kernel, dim3(unsigned(1 + (copiers < 512 ? copiers : 512))),
                      dim3(kOne), 0, st, a);
-  if (forks > 0)
-    hipLaunchKernelGGL(fork_copy_kernel, dim3(unsigned(forks * layers)), dim3(kBlock), 0, st, a);
+  if (forks > 0) {
+    // (threads along x are counted in 32 bits)
+    const int64_t pieces = forks * layers, most = 1 << 22, x = pieces < most ? pieces : most;
+    hipLaunchKernelGGL(fork_copy_kernel, dim3(unsigned(x), unsigned((pieces + x - 1) / x)),
+                       dim3(kBlock), 0, st, a);
+  }
   return launch_status();
 }
 

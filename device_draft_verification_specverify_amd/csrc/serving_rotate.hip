@@ -2,10 +2,11 @@
 // and values into their slots of a paged cache (gfx950).
 //
 // Bytes are all there is to it: every element is read once and written once. A
-// workgroup takes a token: the angles of its position are the same for all heads, so
-// they are taken once (in float64: at position 100000 a float32 product would leave
-// 0.004 of a turn) and held in LDS. A head is DP / 8 lanes of 8 elements each, which
-// sum its squares by lane exchanges and hand each other the second element of a pair.
+// workgroup, or a wavefront where the heads are few, takes a token: the angles of its
+// position are the same for all heads, so they are taken once (in float64: at position
+// 100000 a float32 product would leave 0.004 of a turn) and held in LDS. A head is 8, 16
+// or 32 lanes of 8 elements each, which sum its squares by lane exchanges and hand each
+// other the second element of a pair.
 // 8192 tokens of 32 + 8 heads of 128 and values into the cache (201 MB) 47 us, 4.3 TB/s:
 // 53 us with loads and stores through the caches, which nothing here comes back to, and
 // one set of heads at a time.
@@ -79,19 +80,34 @@ __device__ __forceinline__ void store8(void* p, const Eight<DT>& x) {
   for (int i = 0; i < N; ++i) __builtin_nontemporal_store(raw.w[i], static_cast<u32x4*>(p) + i);
 }
 
+constexpr int64_t kMaxGrid = 1 << 22;  // workgroups along x: threads there are counted in 32 bits
+
 enum { kHalves, kHalvesOdd, kPairs };  // the second element of a pair: R / 2 further on
                                        // (in whole pieces of 8 or not), or the next
 
-template <int DT, int LANES, int MODE>
+// What a wavefront has written to LDS is there for its own lanes.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// G threads take a token: all of the workgroup, or a wavefront.
+template <int DT, int LANES, int MODE, int G>
 __global__ __launch_bounds__(kBlock) void rotate_kernel(RotateArgs a) {
   using elem = typename Type<DT>::type;
-  constexpr int HEADS = kBlock / LANES;  // at once
+  constexpr int HEADS = G / LANES;  // at once
   constexpr int AHEAD = 2;
-  __shared__ float cosines[SV_MAX_HEAD_DIM / 2], sines[SV_MAX_HEAD_DIM / 2];
-  __shared__ float box[MODE == kHalvesOdd ? kBlock * 8 : 1];
-  const int64_t t = blockIdx.x;
-  const int tid = int(threadIdx.x);
-  if (!sv_ok(t < a.T)) return;
+  constexpr int PAD = 9;  // floats of a lane: 8, and one that moves the next lane's banks on
+  __shared__ float all_cosines[kBlock / G][SV_MAX_HEAD_DIM / 2], all_sines[kBlock / G][SV_MAX_HEAD_DIM / 2];
+  __shared__ float box[MODE == kHalvesOdd ? kBlock * PAD : 1];
+  // (the same for a wavefront, and so scalar)
+  const int group = G == kBlock ? 0 : __builtin_amdgcn_readfirstlane(int(threadIdx.x) / G);
+  const int tid = int(threadIdx.x) - group * G;
+  const int64_t t = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * (kBlock / G) + group;
+  if (t >= a.T) return;
+  float* const cosines = all_cosines[group];
+  float* const sines = all_sines[group];
   const int32_t position = a.position[t];
   if (position < 0) return;
   const int in = tid % LANES, d0 = in * 8, half = a.R / 2;
@@ -118,15 +134,16 @@ __global__ __launch_bounds__(kBlock) void rotate_kernel(RotateArgs a) {
   Eight<DT> ahead[AHEAD];
 #pragma unroll
   for (int u = 0; u < AHEAD; ++u) ahead[u] = fetch(u * HEADS + tid / LANES);
-  if (tid < a.R / 2) {
+  for (int j = tid; j < a.R / 2; j += G) {
     // the angle in turns, what is left of it beside whole ones
-    const double turns = double(position) * double(a.inv_freq[tid]) * 0.15915494309189533577;
+    const double turns = double(position) * double(a.inv_freq[j]) * 0.15915494309189533577;
     float s, c;
     sincospif(float(2.0 * (turns - rint(turns))), &s, &c);
-    cosines[tid] = c;
-    sines[tid] = s;
+    cosines[j] = c;
+    sines[j] = s;
   }
-  __syncthreads();
+  if constexpr (G == kWave) wave_sync();
+  else __syncthreads();
   for (int h0 = 0; h0 < heads; h0 += HEADS) {
     const int h = h0 + tid / LANES;
     const Eight<DT> raw = ahead[0];
@@ -139,7 +156,7 @@ __global__ __launch_bounds__(kBlock) void rotate_kernel(RotateArgs a) {
         const int kv = h - a.Hq - a.Hkv;
         store8<DT>(a.v_cache + at + kv * a.c_h + d0 * sizeof(elem), raw);
       }
-      if (MODE != kHalvesOdd) continue;
+      continue;
     }
     const int kv = h - a.Hq;
     float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -190,17 +207,18 @@ __global__ __launch_bounds__(kBlock) void rotate_kernel(RotateArgs a) {
         y.x[i] = elem(first || second ? x[i] * c + z * s : x[i]);
       }
     } else {
-      float* mine = box + (tid - in) * 8;
-      __syncthreads();
+      float* mine = box + (int(threadIdx.x) - in) * PAD;  // the head's, of one wavefront
+      wave_sync();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) mine[d0 + i] = x[i];
-      __syncthreads();
+      for (int i = 0; i < 8; ++i) mine[in * PAD + i] = x[i];
+      wave_sync();
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int d = d0 + i;
         const bool first = d < half, second = !first && d < a.R;
         const int j = first ? d : second ? d - half : 0;
-        const float z = mine[first ? d + half : second ? d - half : d];
+        const int o = first ? d + half : second ? d - half : d;
+        const float z = mine[o + o / 8];
         const float c = cosines[j], s = first ? -sines[j] : sines[j];
         y.x[i] = elem(first || second ? x[i] * c + z * s : x[i]);
       }
@@ -215,12 +233,24 @@ __global__ __launch_bounds__(kBlock) void rotate_kernel(RotateArgs a) {
   }
 }
 
+template <int DT, int LANES, int MODE>
+void launch_threads(const RotateArgs& a, hipStream_t st) {
+  // A wavefront to a token where a workgroup would not be full of its heads: 8000 tokens
+  // of 8 + 1 heads of 128 18 us, 22 us by workgroups; of 32 + 8 heads 56 us, 51 us by
+  // workgroups.
+  const bool wave = int64_t(a.Hq + 2 * int64_t(a.Hkv)) * LANES <= kBlock;
+  const int64_t groups = wave ? (a.T + kBlock / kWave - 1) / (kBlock / kWave) : a.T;
+  const int64_t x = groups < kMaxGrid ? groups : kMaxGrid;
+  const dim3 grid{unsigned(x), unsigned((groups + x - 1) / x), 1u};
+  if (wave) hipLaunchKernelGGL((rotate_kernel<DT, LANES, MODE, kWave>), grid, dim3(kBlock), 0, st, a);
+  else hipLaunchKernelGGL((rotate_kernel<DT, LANES, MODE, kBlock>), grid, dim3(kBlock), 0, st, a);
+}
+
 template <int DT, int LANES>
 void launch_mode(const RotateArgs& a, int mode, hipStream_t st) {
-  const dim3 grid(unsigned(a.T)), block(kBlock);
-  if (mode == kPairs) hipLaunchKernelGGL((rotate_kernel<DT, LANES, kPairs>), grid, block, 0, st, a);
-  else if (mode == kHalves) hipLaunchKernelGGL((rotate_kernel<DT, LANES, kHalves>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((rotate_kernel<DT, LANES, kHalvesOdd>), grid, block, 0, st, a);
+  if (mode == kPairs) launch_threads<DT, LANES, kPairs>(a, st);
+  else if (mode == kHalves) launch_threads<DT, LANES, kHalves>(a, st);
+  else launch_threads<DT, LANES, kHalvesOdd>(a, st);
 }
 
 template <int DT>
