@@ -16,7 +16,8 @@ constexpr int kFewRows = 64;
 
 // What an item costs the kernel whose wavefronts take turns besides its tiles (its
 // rows loaded and written, the masked tiles at its end), in tiles: 8192 tokens from
-// nothing 624 us with 3, 561 us with 6, 547 us with 8, 551 us with 10.
+// nothing 624 us with 3, 561 us with 6, 547 us with 8; on another card 568 us with 7,
+// 570 with 8, 574 with 10.
 constexpr int kTurnPlaces = 8;
 
 struct Variant {

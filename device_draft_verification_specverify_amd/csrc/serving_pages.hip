@@ -135,8 +135,8 @@ __device__ __forceinline__ int find_one(const int32_t* front, int B, int32_t k) 
 // Each thread is a request, then what all requests give back, take and write is
 // shared out over the threads entry by entry. Bound by the trips to memory one
 // after another (lengths, entries, the pages' shares, the list): one request of 2048
-// new tokens 8 us, 64 of up to 600 behind up to 8192 in 16384 pages 17 us; a call's
-// host time is 13 us against 20 us of the kernels below.
+// new tokens 8 us, a call 14.5 us; the four kernels below together are 23 us for 512
+// requests, and their launches alone keep the host longer than this one runs.
 __global__ __launch_bounds__(kOne) void resize_one_kernel(ResizeArgs a) {
   __shared__ uint32_t given[kOnePages];
   __shared__ uint16_t freed[kOnePages];  // the pages that come free, in order
@@ -515,8 +515,8 @@ __device__ __forceinline__ Fork fork_of(const ForkArgs& a, const int32_t* named,
 
 // The first workgroup settles what every fork does, a thread each, in order; the
 // others copy the arrays that the next launch changes in places. (With a launch of
-// its own for each of these, and one for the tables, four replies to one prompt took
-// 23 us of host time rather than 17.)
+// its own for each of these, and one for the tables, a call for four replies to one
+// prompt took 22.5 us rather than 19.6.)
 __global__ __launch_bounds__(kOne) void fork_plan_kernel(ForkArgs a) {
   const int tid = int(threadIdx.x);
   if (blockIdx.x > 0) {
@@ -584,7 +584,7 @@ __global__ __launch_bounds__(kOne) void fork_plan_kernel(ForkArgs a) {
 
 // One workgroup per (fork, layer): the tokens of the last page, keys and values; that
 // of the first layer writes the target's table too. 64 forks of some 16 tokens in 32
-// layers (245 MB): 50 us, 4.9 TB/s.
+// layers (245 MB, many of one source): 35 us, and a call 60 us.
 __global__ __launch_bounds__(kBlock) void fork_copy_kernel(ForkArgs a) {
   const int64_t block = int64_t(blockIdx.y) * gridDim.x + blockIdx.x;
   const int64_t j = block % a.forks, layer = block / a.forks;

@@ -7,9 +7,9 @@
 // 100000 a float32 product would leave 0.004 of a turn) and held in LDS. A head is 8, 16
 // or 32 lanes of 8 elements each, which sum its squares by lane exchanges and hand each
 // other the second element of a pair.
-// 8192 tokens of 32 + 8 heads of 128 and values into the cache (201 MB) 47 us, 4.3 TB/s:
-// 53 us with loads and stores through the caches, which nothing here comes back to, and
-// one set of heads at a time.
+// 8192 tokens of 32 + 8 heads of 128 and values into the cache (201 MB) 44 to 49 us by
+// card, 4.1 to 4.5 TB/s: 51 to 53 us with loads and stores through the caches, which
+// nothing here comes back to, and one set of heads at a time.
 
 #include "specverify_serving.h"
 #include "tree_common.h"
@@ -236,7 +236,7 @@ __global__ __launch_bounds__(kBlock) void rotate_kernel(RotateArgs a) {
 template <int DT, int LANES, int MODE>
 void launch_threads(const RotateArgs& a, hipStream_t st) {
   // A wavefront to a token where a workgroup would not be full of its heads: 8000 tokens
-  // of 8 + 1 heads of 128 18 us, 22 us by workgroups; of 32 + 8 heads 56 us, 51 us by
+  // of 8 + 1 heads of 128 15 us, 18 us by workgroups; of 32 + 8 heads 56 us, 51 us by
   // workgroups.
   const bool wave = int64_t(a.Hq + 2 * int64_t(a.Hkv)) * LANES <= kBlock;
   const int64_t groups = wave ? (a.T + kBlock / kWave - 1) / (kBlock / kWave) : a.T;
